@@ -66,6 +66,10 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_DEV_NONFINITE 2    /* a needed row had a non-finite max or normaliser: accept_len = -1 */
 #define SPEC_DEV_VERIFY_LEN 4   /* verify_len[b] outside [0, L]: accept_len = -1 */
 #define SPEC_DEV_SCORES 8       /* a survival score outside [0, 1] or NaN */
+#define SPEC_DEV_INDEX 16       /* a seat, mask or row offset outside its table, or a seat named twice: request left out */
+#define SPEC_DEV_PARAM 32       /* a penalty that is not finite, or repetition <= 0: request left out */
+#define SPEC_DEV_PAGES 64       /* no free pages, or more than a page-table row holds: request refused */
+#define SPEC_DEV_LENGTHS 128    /* offsets, a length or a page count that cannot be: request or call left out */
 
 /* Limits. */
 #define SPEC_MAX_L 32
@@ -73,6 +77,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_MAX_B 4096
 #define SPEC_MAX_V 1048576      /* vocabulary of the verify calls (terminal token packed in 20 bits) */
 #define SPEC_MAX_DVL_ELEMS 16384 /* B * L for dvl_allocate_pack */
+#define SPEC_MAX_SEATS 65536    /* rows of the per-request state tables */
+#define SPEC_MAX_BIAS 1024      /* bias entries of one seat */
 #define SPEC_NOALLOC_MAX_ROWS 4096 /* rows of spec_softmax_T_noalloc (fixed 48 KiB scratch) */
 
 /* Human-readable name of a spec_status value. Host only; never fails. */
@@ -318,6 +324,161 @@ int dvl_allocate_pack(const float* scores, int B, int L, int budget,
                       int32_t* verify_len, int32_t* offsets, int32_t* slot_map,
                       const void* dense_target, void* packed_target, int dtype, int64_t V,
                       void* workspace, size_t ws_bytes, spec_stream_t stream);
+
+/*
+ * Serving state. A request sits in one "seat" for its life; the tables below
+ * have one row per seat, at fixed addresses, and a step names the seats of
+ * its requests on the device (seats [B] int32; NULL: request b sits in seat
+ * b; negative: no seat, the padding of a batch). The structs live on the
+ * host and are read during the call; the pointers in them are device
+ * pointers. They must not be changed by another stream while a call runs.
+ */
+
+/* What the penalties and biases of a seat are computed from. */
+typedef struct {
+  int32_t* counts;            /* [seats, V] how often the request's output holds the token */
+  uint32_t* seen;             /* [seats, ceil(V/32)] bit v%32 of word v/32: the prompt or the output holds token v;
+                                 set wherever counts is not 0 */
+  const float* repetition;    /* [seats] r > 0 (NULL: 1) */
+  const float* frequency;     /* [seats] f (NULL: 0) */
+  const float* presence;      /* [seats] p (NULL: 0) */
+  const int32_t* bias_tokens; /* [seats, n_bias] (NULL when n_bias == 0); negative: unused entry */
+  const float* bias_values;   /* [seats, n_bias] */
+  int32_t n_bias;             /* 0 ... SPEC_MAX_BIAS */
+  int32_t seats;              /* 1 ... SPEC_MAX_SEATS */
+  int64_t V;
+} spec_history;
+
+/* The pages of a paged cache and who holds them. */
+typedef struct {
+  int32_t* page_table;        /* [seats, max_pages] pages of a seat, in order of position */
+  int32_t* owned;             /* [seats] how many it holds */
+  int32_t* free_pages;        /* [n_pages] stack of free pages; what is at and above free_count is left as it was */
+  int32_t* free_count;        /* [1] */
+  int32_t seats;              /* 1 ... SPEC_MAX_SEATS */
+  int32_t max_pages;          /* columns of page_table */
+  int32_t n_pages;
+  int32_t page_size;          /* tokens of a page, any positive number */
+} spec_kv_pages;
+
+/* Workspaces (spec_workspace_init once, then reused). That of the rules and
+ * history calls holds the status word alone, so overlapping calls and graphs
+ * may share it; that of the kv calls also holds a ticket and may not be
+ * shared by calls that overlap. 0 for B outside 1 ... SPEC_MAX_B. */
+size_t spec_rules_workspace_size(int B);
+size_t spec_kv_workspace_size(int B);
+
+/*
+ * spec_logit_rules — penalties, biases and grammar masks on the logit rows of
+ * a verify step, before spec_verify_* or spec_softmax_T reads them ([DBLAST]
+ * "Assumptions": target and draft are taken under the same sampling filter).
+ * For row i of request b, seat s, with x_0.. the drafted tokens:
+ *   c(v)  = counts[s,v] + #{k < i : x_k = v}
+ *   known = seen[s,v] or v among x_0..x_{i-1}
+ *   z     = known ? (x > 0 ? x / r : x * r) : x
+ *   z     = z - f c(v) - (c(v) > 0 ? p : 0) + sum of the seat's bias values at v
+ *   out   = z, or -inf where the mask's bit v is 0 (whatever x is there)
+ * in fp32, rounded once. Entries of a bias list that name one token add up in
+ * list order.
+ *   logits      [B, K, rows, V] of `dtype`, or packed target rows [n_rows, V]
+ *               with row_off (K == 1): row (b, i) is row_off[b] + i.
+ *   out         same layout; == logits edits in place (only the elements that
+ *               a rule changes are written). Otherwise the two must not
+ *               overlap, and every processed row is written whole.
+ *   rows        L + 1 (target rows: i = 0..l_b) or L (draft rows: i < l_b),
+ *               l_b = verify_len[b] (L if NULL). Rows beyond are left as they
+ *               were. A plain decoding step is L = 0, rows = 1, K = 1.
+ *   n_rows      rows of the buffer (B * K * rows when row_off is NULL).
+ *   draft_tokens [B, L] int32 (NULL allowed when L == 0 or history is NULL).
+ *               A token outside [0, V) raises SPEC_DEV_TOKEN_RANGE and counts
+ *               for nothing.
+ *   history     NULL: no penalties and biases. seats as above; a request
+ *               without a seat has none either.
+ *   mask        [n_masks, mask_len, ceil(V/32)] words (nullable), mask_len >=
+ *               rows: bit v%32 of word v/32 of row i allows token v at
+ *               position i. mask_rows [B] int32: the request's mask, negative
+ *               for none (NULL: mask b, n_masks >= B). Bits past V are
+ *               ignored. A row that allows nothing becomes -inf throughout,
+ *               and verification reports it as SPEC_DEV_NONFINITE.
+ * A request with verify_len outside [0, L], an index outside its table, rows
+ * outside the buffer or a penalty that is no number is left out: its flag is
+ * raised (SPEC_DEV_VERIFY_LEN, _INDEX, _PARAM) and none of its rows written.
+ * Requests of one call must not share rows (they may share seats and masks).
+ *   workspace   >= spec_rules_workspace_size(B) bytes.
+ * Limits: B, K, L, V as spec_verify_mixture.
+ */
+int spec_logit_rules(const void* logits, void* out, int dtype, const int32_t* row_off, int64_t n_rows, int B, int K,
+                     int rows, int L, int64_t V, const int32_t* draft_tokens, const int32_t* verify_len,
+                     const spec_history* history, const int32_t* seats, const uint32_t* mask, int n_masks,
+                     int mask_len, const int32_t* mask_rows, void* workspace, size_t ws_bytes, spec_stream_t stream);
+
+/*
+ * spec_history_add — tokens enter the history of their requests' seats.
+ *   tokens   offsets == NULL: [B, width] int32 (n_tokens = B * width), e.g.
+ *            the out_tokens of a verify call. Otherwise [n_tokens], those of
+ *            request b at offsets[b] .. offsets[b+1] ([B+1] int32, read on
+ *            the device, non-decreasing within [0, n_tokens]; else
+ *            SPEC_DEV_LENGTHS and nothing is done). Negative tokens are
+ *            padding; others outside [0, V) raise SPEC_DEV_TOKEN_RANGE and
+ *            are left out.
+ *   output   1: generated tokens (seen and counted); 0: prompt tokens (seen).
+ * Seats as above (a seat outside the table: SPEC_DEV_INDEX, left out); a seat
+ * may be named more than once. 1 <= B <= SPEC_MAX_B.
+ *
+ * spec_history_clear — empties the seats of a batch (counts and seen bits;
+ * penalties and biases are the caller's).
+ */
+int spec_history_add(const spec_history* history, const int32_t* seats, int B, const int32_t* tokens,
+                     int64_t n_tokens, const int32_t* offsets, int output, void* workspace, size_t ws_bytes,
+                     spec_stream_t stream);
+int spec_history_clear(const spec_history* history, const int32_t* seats, int B, void* workspace, size_t ws_bytes,
+                       spec_stream_t stream);
+
+/*
+ * spec_kv_map — pages, cache slots and block table of a step whose request
+ * lengths live on the device ([DSCALE] Abstract: fixed-address workspaces
+ * carry changing boundaries through verification). With offsets from
+ * dvl_allocate_pack, request b appends its l_b + 1 packed positions behind
+ * the ctx_len[b] tokens it has in the cache; with the cumulative lengths of
+ * prompts it is a prefill.
+ *   ctx_len     [B] int32.
+ *   offsets     [B+1] int32: tokens offsets[b] .. offsets[b+1] are request
+ *               b's; non-decreasing within [0, n_tokens].
+ *   n_tokens    capacity of kv_slots and positions.
+ * A request takes pages from the top of the free stack until it holds
+ * ceil((ctx_len + new) / page_size); requests are served in batch order.
+ *   kv_slots    [n_tokens] int64 out: page * page_size + offset in the page;
+ *               -1 for entries of no (or a refused) request.
+ *   positions   [n_tokens] int32 out (nullable): position in the sequence; 0
+ *               where kv_slots is -1.
+ *   seq_len     [B] int32 out: ctx_len + new; 0 without a seat; -1 refused.
+ *   block_table [B, max_pages] int32 out (nullable): the pages in use, per
+ *               batch row; entries past them are left as they were.
+ * A request is refused, with its pages left as they are, when the pages it
+ * needs (added to those that requests before it asked for) are not free or
+ * exceed max_pages (SPEC_DEV_PAGES), when its seat is outside the table or
+ * named twice (SPEC_DEV_INDEX), or its lengths are impossible
+ * (SPEC_DEV_LENGTHS). Offsets or a free_count outside their range refuse the
+ * whole call (SPEC_DEV_LENGTHS).
+ *
+ * spec_kv_release — gives pages back: each request keeps the pages of its
+ * first keep_len[b] tokens (NULL: none, the request is finished), the others
+ * go onto the free stack in (request, position) order and their page_table
+ * entries become -1. After verification, keep_len = ctx_len + accept_len + 1
+ * takes back what rejected positions held. Requests without a seat are
+ * skipped; seats outside the table or named twice (SPEC_DEV_INDEX) and
+ * impossible lengths (SPEC_DEV_LENGTHS) are left out; a stack that would
+ * overflow leaves the whole call undone (SPEC_DEV_LENGTHS).
+ *
+ * Both: workspace >= spec_kv_workspace_size(B) bytes, 1 <= B <= SPEC_MAX_B,
+ * B * max_pages < 2^31. One launch each; results are functions of the inputs
+ * alone. Calls on one spec_kv_pages must be in stream order.
+ */
+int spec_kv_map(const spec_kv_pages* pages, const int32_t* seats, int B, const int32_t* ctx_len,
+                const int32_t* offsets, int64_t n_tokens, int64_t* kv_slots, int32_t* positions, int32_t* seq_len,
+                int32_t* block_table, void* workspace, size_t ws_bytes, spec_stream_t stream);
+int spec_kv_release(const spec_kv_pages* pages, const int32_t* seats, int B, const int32_t* keep_len,
+                    void* workspace, size_t ws_bytes, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,10 @@ Entry points (same names as the C ABI):
   spec_verify_mixture_top_p(target, draft, mix_w, tokens, u, g, T, top_p, ...)
   spec_verify_window_stats(...), spec_verify_accept(...)   the two verify stages
   dvl_allocate_pack(scores, budget, dense_target=None, packed_target=None)
+  spec_logit_rules(logits, history, ...)                   penalties, biases, grammar masks on the rows of a step
+  spec_history_add(history, tokens, ...), spec_history_clear(history, seats)
+  spec_kv_map(pages, ctx_len, offsets, n_tokens, ...), spec_kv_release(pages, seats, ...)
+State tables of the last two groups: History, KvPages (serving.py).
 Workspaces: Workspace(nbytes, device), with verify/softmax/dvl size helpers;
 Workspace.status() reads the sticky device flags (DEV_*).
 """
@@ -28,12 +32,14 @@ import torch
 __all__ = ["SpecError", "Workspace", "lib", "softmax_T", "spec_softmax_T", "spec_softmax_T_noalloc", "NOALLOC_MAX_ROWS", "spec_verify_block",
            "spec_verify_mixture", "spec_verify_block_top_p", "spec_verify_mixture_top_p",
            "verify_top_p_workspace_size", "spec_verify_window_stats", "spec_verify_accept", "dvl_allocate_pack", "verify_workspace_size", "softmax_workspace_size",
-           "dvl_workspace_size", "check_verify_args", "LIB_PATH", "EXPORTS", "DEV_TOKEN_RANGE", "DEV_NONFINITE", "DEV_VERIFY_LEN",
-           "DEV_SCORES"]
+           "dvl_workspace_size", "History", "KvPages", "spec_logit_rules", "spec_history_add", "spec_history_clear",
+           "spec_kv_map", "spec_kv_release", "rules_workspace_size", "kv_workspace_size", "check_verify_args", "LIB_PATH", "EXPORTS", "DEV_TOKEN_RANGE", "DEV_NONFINITE", "DEV_VERIFY_LEN",
+           "DEV_SCORES", "DEV_INDEX", "DEV_PARAM", "DEV_PAGES", "DEV_LENGTHS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libspecv.so")
 
 DEV_TOKEN_RANGE, DEV_NONFINITE, DEV_VERIFY_LEN, DEV_SCORES = 1, 2, 4, 8
+DEV_INDEX, DEV_PARAM, DEV_PAGES, DEV_LENGTHS = 16, 32, 64, 128
 NOALLOC_MAX_ROWS = 4096  # SPEC_NOALLOC_MAX_ROWS
 _F32, _BF16 = 0, 1
 
@@ -55,6 +61,13 @@ _SIGS = {
     "spec_verify_window_stats": ([_P, _P, _P, _I, _I, _P, _P, _I, _I, _I64, _F, _P, _SZ, _P], _I),
     "spec_verify_accept": ([_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I64, _F, _P, _P, _P, _SZ, _P], _I),
     "dvl_allocate_pack": ([_P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I64, _P, _SZ, _P], _I),
+    "spec_rules_workspace_size": ([_I], _SZ),
+    "spec_kv_workspace_size": ([_I], _SZ),
+    "spec_logit_rules": ([_P, _P, _I, _P, _I64, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _I, _I, _P, _P, _SZ, _P], _I),
+    "spec_history_add": ([_P, _P, _I, _P, _I64, _P, _I, _P, _SZ, _P], _I),
+    "spec_history_clear": ([_P, _P, _I, _P, _SZ, _P], _I),
+    "spec_kv_map": ([_P, _P, _I, _P, _P, _I64, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "spec_kv_release": ([_P, _P, _I, _P, _P, _SZ, _P], _I),
 }
 EXPORTS = tuple(_SIGS)
 
@@ -403,3 +416,7 @@ def dvl_allocate_pack(scores, budget, *, dense_target=None, packed_target=None, 
           _dev(vl, "verify_len", torch.int32), _dev(off, "offsets", torch.int32),
           _opt(sm, "slot_map", torch.int32), dptr, pptr, dt, V, ws.ptr(), ws.nbytes, _stream(scores))
     return vl, off, sm
+
+
+from .serving import (History, KvPages, kv_workspace_size, rules_workspace_size, spec_history_add,  # noqa: E402
+                      spec_history_clear, spec_kv_map, spec_kv_release, spec_logit_rules)

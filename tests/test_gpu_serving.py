@@ -1,0 +1,625 @@
+"""Serving operators on the GPU against the plain 64-bit definitions
+(oracle/serving.py).
+
+Tolerance of an edited logit. The kernel computes
+z = fl(fl(fl(x / r) - f c) - p) + bias in fp32. Each of its at most 4 + n_b
+operations (n_b bias entries of one token, 8 at most here) rounds a value no
+larger than S = |x / r or x r| + |f| c + |p| + sum |bias|, by 2^-24 of it; the
+parameters are the same fp32 numbers on both sides. So |z_gpu - z| <= E =
+12 * 2^-24 * S, and the final rounding adds half a step of the type, 2^-8
+(bf16) or 0 (fp32: z is already fp32) of |z| + E. Elements that no rule names
+must keep their bits. Whole numbers (counts, bits, slots, tables) are equal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import speculative_decoding_block_spec_b200 as specv
+from oracle import serving as plain
+from speculative_decoding_block_spec_b200 import synth
+from speculative_decoding_block_spec_b200.synth import f32_to_bf16_bits
+
+from parity_util import check_verify, logits_to_torch
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="no CUDA device")]
+I32 = torch.int32
+
+
+def dev(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def words(a):
+    return dev(np.ascontiguousarray(a).view(np.int32))
+
+
+def host(t):
+    """bf16 as bit patterns, else as is."""
+    if t.dtype == torch.bfloat16:
+        return t.view(torch.int16).cpu().numpy().view(np.uint16)
+    return t.cpu().numpy()
+
+
+def to_type(x, dtype):
+    return f32_to_bf16_bits(x) if dtype == "bf16" else x.astype(np.float32)
+
+
+class Case:
+    """Random rows, histories, penalties, biases and masks of one call."""
+
+    def __init__(self, seed, B, K, L, V, *, rows, dtype="bf16", packed=False, hist=50, bias=0, mask=None, seats=True,
+                 vlen=True, params=True):
+        g = np.random.default_rng(seed)
+        self.B, self.K, self.L, self.V, self.rows, self.dtype = B, K, L, V, rows, dtype
+        self.vlen = g.integers(0, L + 1, B).astype(np.int32) if vlen else None
+        self.row_off, n = None, B * K * rows
+        if packed:
+            ln = (self.vlen if vlen else np.full(B, L)) + 1
+            self.row_off = (np.cumsum(ln) - ln + 1).astype(np.int32)  # a row before the first: must stay as it was
+            n = int(ln.sum()) + 3
+        self.x = to_type(g.standard_normal((n, V)).astype(np.float32) * 3, dtype)
+        self.tokens = g.integers(0, min(V, 40), (B, L)).astype(np.int32)  # few ids: repeats, also of seen tokens
+        self.kw, self.seats = {}, None
+        if hist is not None:
+            S = B + 3
+            if seats:
+                self.seats = g.permutation(S)[:B].astype(np.int32)
+                if B > 2:
+                    self.seats[1], self.seats[2] = -1, self.seats[0]  # no seat; one seat read by two requests
+            counts = np.zeros((S, V), np.int32)
+            seen = np.zeros((S, V), bool)
+            for s in range(S):
+                ids = g.integers(0, V, hist) if s % 2 else g.integers(0, min(V, 3 * hist + 1), hist)
+                seen[s, ids] = True
+                np.add.at(counts[s], ids[: hist // 2], 1)
+            counts[0, ids[:1]] = 70000
+            self.kw.update(counts=counts, seen=plain.pack_bits(seen))
+            if params:
+                self.kw.update(repetition=g.uniform(0.7, 1.5, S).astype(np.float32),
+                               frequency=g.uniform(-0.5, 1, S).astype(np.float32),
+                               presence=g.uniform(-0.5, 1, S).astype(np.float32))
+            if bias:
+                bt = g.integers(0, V, (S, bias)).astype(np.int32)
+                bt[:, bias // 2] = bt[:, 0]              # one token twice
+                bt[g.random((S, bias)) < 0.1] = -1
+                self.kw.update(bias_tokens=bt, bias_values=(g.standard_normal((S, bias)) * 4).astype(np.float32))
+        self.mask = self.mask_rows = None
+        if mask:
+            M = B if mask == "own" else max(1, B // 2)
+            ok = g.random((M, rows + 1, V)) < g.choice([0.01, 0.5, 0.99], (M, rows + 1, 1))
+            ok[0, 0] = False                             # a row that allows nothing
+            ok[-1, -1] = True
+            self.mask = plain.pack_bits(ok)
+            if V % 32:                                   # bits past V mean nothing
+                self.mask[..., -1] |= np.uint32(0xffffffff << (V % 32) & 0xffffffff)
+            if mask != "own":
+                self.mask_rows = g.integers(-1, M, B).astype(np.int32)
+
+    def oracle(self):
+        return plain.logit_rules(self.x, self.B, self.K, self.rows, self.L, row_off=self.row_off, tokens=self.tokens,
+                                 verify_len=self.vlen, seats=self.seats, mask=self.mask, mask_rows=self.mask_rows,
+                                 **self.kw)
+
+    def history(self):
+        k = self.kw
+        if not k:
+            return None
+        return specv.History(dev(k["counts"]), words(k["seen"]), dev(k.get("repetition")), dev(k.get("frequency")),
+                             dev(k.get("presence")), dev(k.get("bias_tokens")), dev(k.get("bias_values")))
+
+    def view(self, t):
+        return t if self.row_off is not None else t.view(self.B, self.K, self.rows, self.V)
+
+    def call(self, x, out=None, **kw):
+        args = dict(seats=dev(self.seats), draft_tokens=dev(self.tokens), verify_len=dev(self.vlen),
+                    target_row_off=dev(self.row_off), mask=None if self.mask is None else words(self.mask),
+                    mask_rows=dev(self.mask_rows), out=out)
+        args.update(kw)
+        return specv.spec_logit_rules(x, self.history(), **args)
+
+
+def check_rows(got, x, ref, dtype, before=None):
+    """got, x: host rows; before: what the rows that are not processed hold."""
+    before = x if before is None else before
+    done = ref["done"]
+    np.testing.assert_array_equal(got[~done], before[~done])
+    keep = done[:, None] & ~ref["touched"]
+    np.testing.assert_array_equal(got[keep], x[keep])
+    z, y = ref["z"], plain.widen(got)
+    edit = done[:, None] & ref["touched"]
+    e = 12 * 2.0 ** -24 * ref["size"]
+    h = 2.0 ** -8 if dtype == "bf16" else 0.0
+    fine = edit & np.isfinite(z)
+    with np.errstate(invalid="ignore"):
+        bound = h * (np.abs(z) + e) + e
+    bad = np.abs(y[fine] - z[fine]) > bound[fine]
+    assert not bad.any(), (z[fine][bad][:5], y[fine][bad][:5])
+    np.testing.assert_array_equal(y[edit & ~np.isfinite(z)], z[edit & ~np.isfinite(z)])
+
+
+SHAPES = [
+    dict(B=1, K=1, L=0, V=64, rows=1),
+    dict(B=3, K=1, L=0, V=1, rows=1, hist=1),
+    dict(B=5, K=1, L=0, V=1025, rows=1, bias=3),
+    dict(B=3, K=1, L=4, V=257, rows=5, bias=7, mask="own"),
+    dict(B=3, K=1, L=4, V=1000, rows=5, bias=1, mask="some"),
+    dict(B=3, K=1, L=4, V=1001, rows=5, packed=True, bias=5, mask="some", hist=900),
+    dict(B=4, K=3, L=5, V=4096, rows=5, bias=40, mask="some", hist=4000),
+    dict(B=4, K=2, L=5, V=4095, rows=6, bias=40, mask="some"),          # branches of target rows
+    dict(B=2, K=8, L=3, V=2048, rows=3, mask="own", hist=None),
+    dict(B=2, K=1, L=32, V=300, rows=33, bias=20, hist=200),
+    dict(B=2, K=1, L=32, V=8192, rows=33, packed=True, mask="own", hist=8000),
+    dict(B=2, K=1, L=2, V=50257, rows=3, bias=300, mask="own", hist=3000),
+    dict(B=3, K=1, L=2, V=65536, rows=3, bias=1024, hist=30, seats=False, vlen=False),
+    dict(B=2, K=1, L=1, V=151936, rows=2, bias=64, mask="some", hist=5000),
+    dict(B=6, K=1, L=2, V=640, rows=3, bias=6, params=False),           # NULL penalties: biases alone
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", range(len(SHAPES)))
+def test_rules_match_the_definition(n, dtype):
+    c = Case(100 + n, dtype=dtype, **SHAPES[n])
+    ref = c.oracle()
+    assert ref["flags"] == 0 and ref["done"].any()
+    ws = specv.Workspace(specv.rules_workspace_size(c.B))
+    x = c.view(logits_to_torch(c.x))
+    y = c.view(logits_to_torch(to_type(np.full(c.x.shape, 7.0, np.float32), dtype)))
+    before = host(y).reshape(c.x.shape).copy()
+    assert c.call(x, out=y, workspace=ws) is y
+    check_rows(host(y).reshape(c.x.shape), c.x, ref, dtype, before)
+    np.testing.assert_array_equal(host(x).reshape(c.x.shape), c.x)      # out of place: the input stays
+    assert c.call(x, workspace=ws) is x
+    check_rows(host(x).reshape(c.x.shape), c.x, ref, dtype)
+    np.testing.assert_array_equal(host(x)[..., :], host(torch.where(torch.from_numpy(ref["done"]).cuda().view(
+        x.shape[:-1] + (1,)), y, x))) if c.row_off is None else None    # both forms give the same bits
+    assert ws.status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [1, 3])
+def test_rules_on_rows_at_odd_addresses(dtype, shift):
+    """V keeps 16-byte rows, the buffers' addresses do not."""
+    c = Case(7, 3, 1, 4, 1024, rows=5, dtype=dtype, bias=9, mask="own")
+    ref = c.oracle()
+    n = c.x.size
+    for out_shift in (None, shift, 0, 2):
+        big = logits_to_torch(np.concatenate([c.x.ravel()[:shift], c.x.ravel(), c.x.ravel()[:4]]))
+        x = big[shift:shift + n].view(c.B, 1, c.rows, c.V)
+        if out_shift is None:
+            c.call(x)
+            check_rows(host(x).reshape(c.x.shape), c.x, ref, dtype)
+        else:
+            buf = torch.full((n + 8,), 5.0, dtype=x.dtype, device="cuda")
+            y = buf[out_shift:out_shift + n].view(x.shape)
+            before = host(y).reshape(c.x.shape).copy()
+            c.call(x, out=y)
+            check_rows(host(y).reshape(c.x.shape), c.x, ref, dtype, before)
+            assert torch.all(buf[:out_shift] == 5.0) and torch.all(buf[out_shift + n:] == 5.0)
+        assert torch.equal(big[:shift].float().cpu(), torch.from_numpy(
+            plain.widen(c.x.ravel()[:shift])).float())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rules_on_infinities_and_nan(dtype):
+    c = Case(11, 2, 1, 2, 300, rows=3, dtype=dtype, hist=150, bias=4, mask="own", vlen=False, seats=False)
+    x = plain.widen(c.x).astype(np.float32)
+    x[:, ::7], x[:, 1::7], x[:, 2::7] = -np.inf, np.nan, np.inf
+    x[:, 3::7] = np.finfo(np.float32).min if dtype == "f32" else -3.3895314e38
+    c.x = to_type(x, dtype)
+    c.kw["repetition"][:] = 1.25                      # the lowest value times r: -inf in fp32
+    ref = c.oracle()
+    with np.errstate(over="ignore"):
+        z32 = ref["z"].astype(np.float32).astype(np.float64)
+    y = logits_to_torch(c.x).view(2, 1, 3, 300)
+    c.call(y)
+    got = plain.widen(host(y).reshape(c.x.shape))
+    edit = ref["touched"] & ref["done"][:, None]
+    np.testing.assert_array_equal(np.isnan(got[edit]), np.isnan(z32[edit]))
+    allowed = plain.bits_of(c.mask, 300)[:, :3].reshape(-1, 300)
+    assert np.all(got[~allowed] == -np.inf)           # NaN and +inf under the mask too
+    # near the type's limit a rounding decides between the largest value and infinity: compared away from it
+    far = edit & (np.abs(z32) < 1e38)
+    e = 12 * 2.0 ** -24 * ref["size"]
+    h = 2.0 ** -8 if dtype == "bf16" else 0.0
+    assert np.all(np.abs(got[far] - z32[far]) <= (h * (np.abs(z32) + e) + 2 * e)[far])
+    inf = edit & np.isinf(z32) & (np.isinf(x) | (np.abs(ref["z"]) > 3.5e38))
+    np.testing.assert_array_equal(got[inf], z32[inf])
+
+
+def test_rules_leave_out_what_they_cannot_do():
+    base = dict(B=5, K=1, L=3, V=700, rows=4, dtype="f32", bias=5, mask="some")
+
+    def run(change, want, packed=False):
+        c = Case(21, packed=packed, **base)
+        c.seats, c.mask_rows = np.arange(5, dtype=np.int32), np.array([0, 1, -1, 1, 0], np.int32)
+        change(c)
+        ref = c.oracle()
+        assert ref["flags"] == want
+        for inplace in (True, False):
+            ws = specv.Workspace(256)
+            x = c.view(logits_to_torch(c.x))
+            y = x if inplace else torch.full_like(x, 3.0)
+            before = host(y).reshape(c.x.shape).copy()
+            c.call(x, out=y, workspace=ws)
+            check_rows(host(y).reshape(c.x.shape), c.x, ref, "f32", before)
+            assert ws.status() == want
+
+    def put(name, at, value):
+        return lambda c: c.kw[name].__setitem__(at, value)
+
+    run(lambda c: c.vlen.__setitem__(2, 4), specv.DEV_VERIFY_LEN)
+    run(lambda c: c.vlen.__setitem__(2, -1), specv.DEV_VERIFY_LEN)
+    run(lambda c: c.seats.__setitem__(1, 8), specv.DEV_INDEX)
+    run(lambda c: c.mask_rows.__setitem__(3, 2), specv.DEV_INDEX)
+    for v in (0.0, -1.0, np.nan, np.inf):
+        run(put("repetition", 3, v), specv.DEV_PARAM)
+    run(put("frequency", 0, np.nan), specv.DEV_PARAM)
+    run(put("presence", 4, -np.inf), specv.DEV_PARAM)
+    run(lambda c: (c.vlen.fill(3), c.tokens.__setitem__((1, 0), 700), c.tokens.__setitem__((2, 1), -5)), specv.DEV_TOKEN_RANGE)
+    run(lambda c: c.kw["bias_tokens"].__setitem__((2, 1), 700), specv.DEV_TOKEN_RANGE)
+    run(lambda c: c.row_off.__setitem__(0, -1), specv.DEV_INDEX, packed=True)
+    run(lambda c: c.row_off.__setitem__(4, c.x.shape[0] - c.vlen[4]), specv.DEV_INDEX, packed=True)
+
+
+def test_rules_neutral_call_writes_nothing():
+    c = Case(5, 2, 1, 2, 500, rows=3, dtype="bf16")
+    c.kw["repetition"][:], c.kw["frequency"][:], c.kw["presence"][:] = 1, 0, 0
+    x = logits_to_torch(c.x).view(2, 1, 3, 500)
+    c.call(x)
+    np.testing.assert_array_equal(host(x).reshape(c.x.shape), c.x)
+    y = torch.zeros_like(x)
+    specv.spec_logit_rules(x, out=y, draft_tokens=dev(c.tokens))         # no rules at all: a copy
+    assert torch.equal(x, y)
+
+
+def test_a_row_that_allows_nothing_is_reported_by_verification():
+    B, L, V = 2, 3, 512
+    x = synth.custom(B=B, L=L, V=V, T=1.0, dtype="f32", seed=3, cid=700)
+    target, draft = logits_to_torch(x.target), logits_to_torch(x.draft)
+    ok = np.ones((1, L + 1, V), bool)
+    ok[0, 0] = False
+    specv.spec_logit_rules(target, draft_tokens=dev(x.tokens), mask=words(plain.pack_bits(ok)),
+                           mask_rows=dev(np.array([-1, 0], np.int32)))
+    ws = specv.Workspace(specv.verify_workspace_size(B, L, 1, V))
+    acc, _ = specv.spec_verify_block(target, draft, dev(x.tokens), dev(x.u), dev(x.g), 1.0, workspace=ws)
+    assert acc[0] >= 0 and acc[1] == -1 and ws.status() == specv.DEV_NONFINITE
+
+
+def test_rules_past_32_bit_offsets():
+    """State tables and logits of more than 2^31 elements."""
+    V, S = 151936, 15000
+    counts = torch.zeros((S, V), dtype=I32, device="cuda")
+    seen = torch.zeros((S, V // 32), dtype=I32, device="cuda")
+    counts[S - 1, V - 1], seen[S - 1, V // 32 - 1] = 3, -2 ** 31
+    h = specv.History(counts, seen, frequency=torch.full((S,), 0.5, device="cuda"))
+    B, L = 880, 16
+    x = torch.ones((B, L + 1, V), dtype=torch.bfloat16, device="cuda")   # 2.27e9 elements
+    tok = torch.zeros((B, L), dtype=I32, device="cuda")
+    seats = torch.full((B,), -1, dtype=I32, device="cuda")
+    seats[B - 1] = S - 1
+    specv.spec_logit_rules(x, h, seats=seats, draft_tokens=tok)
+    assert x[B - 1, 5, V - 1] == -0.5 and x[B - 1, 5, 0] == 1 - 2.5 and x[B - 1, 16, 0] == -7
+    x[B - 1, :, V - 1], x[B - 1, :, 0] = 1, 1
+    assert bool(torch.all(x == 1))
+    specv.spec_history_add(h, torch.tensor([[V - 1]], dtype=I32, device="cuda"), seats=seats[B - 1:])
+    assert counts[S - 1, V - 1] == 4
+    specv.spec_history_clear(h, seats[B - 1:])
+    assert counts[S - 1, V - 1] == 0 and int(seen.count_nonzero()) == 0
+
+
+# ------------------------------------------------------------------ history
+
+@pytest.mark.parametrize("V", [1, 33, 1000, 50257])
+@pytest.mark.parametrize("output", [True, False])
+def test_history_matches_the_definition(V, output):
+    g = np.random.default_rng(V)
+    S, B = 6, 9
+    seats = np.array([0, 3, 3, -1, 5, 9, 1, 3, 0], np.int32)             # twice, none, outside
+    counts = np.zeros((S, V), np.int32)
+    seen = np.zeros((S, (V + 31) // 32), np.uint32)
+    h, ws = specv.History(dev(counts), words(seen)), specv.Workspace(256)
+    # padded rows
+    toks = g.integers(-1, min(V + 1, 2 ** 31 - 1), (B, 17)).astype(np.int32)
+    counts, seen, f1 = plain.history_add(counts, seen, seats, toks, output)
+    specv.spec_history_add(h, dev(toks), seats=dev(seats), output=output, workspace=ws)
+    # ragged, with empty requests and tokens before the first and behind the last
+    n = np.array([0, 700, 1, 3, 0, 40, 2500, 0, 5])
+    off = (np.concatenate([[0], np.cumsum(n)]) + 4).astype(np.int32)
+    flat = g.integers(0, V, off[-1] + 11).astype(np.int32)
+    flat[5:300] = 0                                                      # one token many times
+    counts, seen, f2 = plain.history_add(counts, seen, seats, [flat[off[b]:off[b + 1]] for b in range(B)], output)
+    specv.spec_history_add(h, dev(flat), offsets=dev(off), seats=dev(seats), output=output, workspace=ws)
+    np.testing.assert_array_equal(h.counts.cpu().numpy(), counts)
+    np.testing.assert_array_equal(h.seen.cpu().numpy().view(np.uint32), seen)
+    assert ws.status() == f1 | f2
+    # empty calls
+    specv.spec_history_add(h, dev(toks[:, :0]), seats=dev(seats))
+    specv.spec_history_add(h, dev(flat[:0]), offsets=dev(np.zeros(B + 1, np.int32)), seats=dev(seats))
+    # clear two seats (one twice), keep the others
+    specv.spec_history_clear(h, dev(np.array([3, -1, 3, 7, 0], np.int32)), workspace=ws)
+    counts[[0, 3]], seen[[0, 3]] = 0, 0
+    np.testing.assert_array_equal(h.counts.cpu().numpy(), counts)
+    np.testing.assert_array_equal(h.seen.cpu().numpy().view(np.uint32), seen)
+
+
+@pytest.mark.parametrize("off", [[0, 5, 4, 8], [-1, 2, 4, 8], [0, 2, 4, 9], [3, 2, 2, 2]])
+def test_history_refuses_bad_offsets(off):
+    h, ws = specv.History.empty(3, 100), specv.Workspace(256)
+    specv.spec_history_add(h, torch.ones(8, dtype=I32, device="cuda"), offsets=dev(np.array(off, np.int32)), workspace=ws)
+    assert ws.status() == specv.DEV_LENGTHS and int(h.counts.sum()) == 0 and int(h.seen.sum()) == 0
+
+
+# ---------------------------------------------------------------------- kv
+
+class Kv:
+    """The library's tables beside the definition's lists."""
+
+    def __init__(self, seats, max_pages, n_pages, ps, B, N, ids=None, block_table=True, positions=True):
+        free = np.random.default_rng(1).permutation(n_pages) if ids is None else np.asarray(ids)
+        self.plain = plain.Pages(seats, max_pages, free, ps)
+        self.pages = specv.KvPages.empty(seats, max_pages, n_pages, ps)
+        self.pages.free_pages.copy_(dev(free.astype(np.int32)))
+        self.ws, self.N = specv.Workspace(specv.kv_workspace_size(B)), N
+        self.bt = torch.full((B, max_pages), -9, dtype=I32, device="cuda") if block_table else None
+        self.bt_want = np.full((B, max_pages), -9, np.int32)
+        self.out = (torch.empty(N, dtype=torch.int64, device="cuda"),
+                    torch.empty(N, dtype=I32, device="cuda") if positions else None,
+                    torch.empty(B, dtype=I32, device="cuda"))
+
+    def map(self, ctx, off, seats):
+        r = self.plain.map(ctx, off, self.N, seats)
+        specv.spec_kv_map(self.pages, dev(np.array(ctx, np.int32)), dev(np.array(off, np.int32)), self.N,
+                          seats=None if seats is None else dev(np.array(seats, np.int32)), block_table=self.bt,
+                          out=self.out, workspace=self.ws)
+        np.testing.assert_array_equal(self.out[0].cpu().numpy(), r["slots"])
+        if self.out[1] is not None:
+            np.testing.assert_array_equal(self.out[1].cpu().numpy(), r["positions"])
+        np.testing.assert_array_equal(self.out[2].cpu().numpy(), r["seq_len"])
+        for b, t in enumerate(r["tables"]):
+            self.bt_want[b, :len(t)] = t
+        if self.bt is not None:
+            np.testing.assert_array_equal(self.bt.cpu().numpy(), self.bt_want)
+        self.same(r["flags"])
+        return r
+
+    def release(self, seats, keep=None):
+        f = self.plain.release(seats, keep)
+        specv.spec_kv_release(self.pages, dev(np.array(seats, np.int32)),
+                              keep_len=None if keep is None else dev(np.array(keep, np.int32)), workspace=self.ws)
+        self.same(f)
+
+    def same(self, flags):
+        p = self.pages
+        n = int(p.free_count)
+        assert p.free_pages[:n].tolist() == self.plain.stack
+        table, owned = p.page_table.cpu().numpy(), p.owned.tolist()
+        for s, held in enumerate(self.plain.held):
+            assert owned[s] == len(held) and table[s, :len(held)].tolist() == held
+            assert np.all(table[s, len(held):] == -1)
+        assert self.ws.status() == flags
+        self.ws.init()
+
+
+@pytest.mark.parametrize("ps,seats,max_pages,n_pages", [(16, 12, 40, 200), (1, 6, 300, 900), (48, 12, 9, 60), (7, 40, 1500, 4000)])
+def test_kv_steps_match_the_definition(ps, seats, max_pages, n_pages):
+    """Admission, decoding with rejected positions, finished requests, padding, shortage of pages."""
+    g = np.random.default_rng(ps)
+    B = min(seats, 8)
+    N = 600
+    kv = Kv(seats, max_pages, n_pages, ps, B, N, block_table=ps != 1, positions=ps != 48)
+    ctx = np.zeros(seats, np.int64)
+    seen = set()
+    for step in range(25):
+        batch = g.permutation(seats)[:B].astype(np.int32)
+        batch[g.random(B) < 0.15] = -1
+        new = np.where(g.random(B) < 0.3, g.integers(0, 130, B), g.integers(0, 18, B))
+        off = np.concatenate([[0], np.cumsum(new)])
+        if off[-1] > N:
+            new[:] = 3
+            off = np.concatenate([[0], np.cumsum(new)])
+        off = off + (step % 3 if off[-1] + 2 <= N else 0)
+        c = np.where(batch >= 0, ctx[batch], 0)
+        r = kv.map(c, off, batch)
+        seen.add(r["flags"])
+        got = np.array(r["seq_len"])
+        keep = np.where(got > 0, np.minimum(got, c + g.integers(0, 6, B)), c)
+        kv.release(batch, keep)
+        for b in range(B):
+            if batch[b] >= 0:
+                ctx[batch[b]] = keep[b]
+        done = batch[(g.random(B) < 0.2) & (batch >= 0)]
+        if len(done):
+            kv.release(done)
+            ctx[done] = 0
+    assert 0 in seen
+
+
+def test_kv_runs_out_of_pages():
+    kv = Kv(4, 8, 10, 4, 4, 64)
+    kv.map([0, 0, 0, 0], [0, 16, 32, 48, 49], None)       # 4 + 4 pages, then 4 of 2 left, then none for the last
+    assert kv.out[2].tolist() == [16, 16, -1, -1]
+    kv.release([1], [5])
+    kv.map([16, 5, 0, 0], [0, 0, 3, 19, 20], None)
+    kv.map([16, 5, 0, 0], [0, 17, 20, 20, 20], None)      # 33 tokens: 9 pages, more than a row holds
+    assert kv.out[2].tolist() == [-1, 8, 0, 0]
+    kv.release([0, 1, 2, 3])
+    assert int(kv.pages.free_count) == 10
+
+
+def test_kv_refusals():
+    kv = Kv(4, 8, 20, 4, 4, 16)
+    kv.map([0, 0, 0, 0], [0, 4, 8, 12, 16], [0, 1, 1, 3])             # a seat named twice
+    kv.map([4, 0, 0, -1], [0, 1, 2, 3, 4], [0, 4, 2, 3])              # outside the table; an impossible length
+    kv.map([0, 0, 0, 2 ** 31 - 1], [0, 1, 2, 3, 4], [0, 1, 2, 3])     # the sum passes 32 bits
+    for off in ([0, 4, 3, 8, 9], [0, 1, 2, 3, 17], [-1, 0, 1, 2, 3]):
+        kv.map([0, 0, 0, 0], off, [0, 1, 2, 3])
+        assert kv.out[2].tolist() == [-1] * 4
+    kv.release([0, 0, 2, -1])                                         # twice: left out
+    kv.release([0, 4, 2, 1], [-1, 0, 1, 1])
+    kv.pages.free_count.fill_(20)                                     # a stack that has no room for what comes back
+    kv.plain.stack = kv.pages.free_pages.tolist()
+    kv.release([0, 1, 2, 3])
+    kv.pages.free_count.fill_(21)
+    specv.spec_kv_map(kv.pages, torch.zeros(4, dtype=I32, device="cuda"), torch.arange(5, dtype=I32, device="cuda"), 16,
+                      out=kv.out, workspace=kv.ws)
+    assert kv.ws.status() == specv.DEV_LENGTHS and kv.out[2].tolist() == [-1] * 4 and set(kv.out[0].tolist()) == {-1}
+
+
+def test_kv_many_requests_and_long_caches():
+    """B at its limit with no tokens for many; page numbers whose slots pass 32 bits; 100,000 tokens in one request."""
+    B = specv_max_b = 4096
+    kv = Kv(65536, 3, 9000, 64, B, 8192, ids=2 ** 31 - 1 - np.arange(9000))
+    g = np.random.default_rng(0)
+    seats = g.permutation(65536)[:specv_max_b]
+    off = np.concatenate([[0], np.cumsum(g.integers(0, 3, B))])
+    off = np.minimum(off, 8192)
+    r = kv.map(g.integers(0, 60, B), off, seats)
+    assert max(r["slots"]) > 2 ** 36
+    kv.release(seats)
+    kv = Kv(2, 8000, 9000, 16, 2, 120000)
+    kv.map([0, 5], [0, 100000, 100017], None)
+    kv.release([0, 1], [99999, 21])
+
+
+# ----------------------------------------------------------- a run of them
+
+def _step_tables(B, L, V, K, S, page, budget, g):
+    """Device buffers of one serving step, at fixed addresses."""
+    x = synth.custom(B=B, L=L, V=V, K=K, T=1.1, dtype="bf16", n_peaks=6, peak=6.0, draft_sigma=0.6, budget=budget,
+                     seed=31, cid=710)
+    d = dict(target=logits_to_torch(x.target), draft=logits_to_torch(x.draft), tokens=dev(x.tokens), u=dev(x.u),
+             g=dev(x.g), mix_w=dev(x.mix_w), scores=dev(x.scores))
+    return x, d
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_serving_step(graph):
+    """Allocation, paging, rules on target and draft, verification, history and release, over several steps with
+    changing data; captured once and replayed, or launched call by call."""
+    B, L, V, K, S, page = 6, 8, 4096, 2, 9, 16
+    budget = B * (L + 1) // 2
+    g = np.random.default_rng(5)
+    x, d = _step_tables(B, L, V, K, S, page, budget, g)
+    seats_h = np.array([4, 0, 7, 2, 8, 5], np.int32)
+    h = specv.History.empty(S, V, 4)
+    h.repetition.copy_(dev(g.uniform(1, 1.4, S).astype(np.float32)))
+    h.frequency.copy_(dev(g.uniform(0, 0.6, S).astype(np.float32)))
+    h.presence.copy_(dev(g.uniform(0, 0.6, S).astype(np.float32)))
+    h.bias_tokens.copy_(dev(g.integers(0, V, (S, 4)).astype(np.int32)))
+    h.bias_values.copy_(dev(g.standard_normal((S, 4)).astype(np.float32)))
+    pages = specv.KvPages.empty(S, 40, 300, page)
+    model = plain.Pages(S, 40, np.arange(299, -1, -1), page)
+    ctx_h = g.integers(20, 60, B).astype(np.int32)
+    prompts = [g.integers(0, V, n).astype(np.int32) for n in ctx_h]
+    off0 = np.concatenate([[0], np.cumsum(ctx_h)]).astype(np.int32)
+    seats = dev(seats_h)
+    specv.spec_history_add(h, dev(np.concatenate(prompts)), offsets=dev(off0), seats=seats, output=False)
+    specv.spec_kv_map(pages, torch.zeros(B, dtype=I32, device="cuda"), dev(off0), int(off0[-1]), seats=seats)
+    model.map([0] * B, off0, int(off0[-1]), seats_h)
+    ok = g.random((2, L + 1, V)) < 0.7
+    ok_d, mask_rows = words(plain.pack_bits(ok)), dev(np.array([-1, 1, -1, 0, -1, -1], np.int32))
+    ctx = dev(ctx_h)
+    packed = torch.empty((budget, V), dtype=torch.bfloat16, device="cuda")
+    draft = torch.empty_like(d["draft"])
+    e = lambda *s, dt=I32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    dvl = (e(B), e(B + 1), e(budget))
+    kv_out, bt = (e(budget, dt=torch.int64), e(budget), e(B)), torch.full((B, 40), -1, dtype=I32, device="cuda")
+    ver = (e(B), e(B, L + 1))
+    keep = e(B)
+    ws = dict(dvl=specv.Workspace(specv.dvl_workspace_size(B)), ver=specv.Workspace(specv.verify_workspace_size(B, L, K, V)),
+              rules=specv.Workspace(specv.rules_workspace_size(B)), kv=specv.Workspace(specv.kv_workspace_size(B)))
+
+    def step():
+        vl, off, _ = specv.dvl_allocate_pack(d["scores"], budget, dense_target=d["target"], packed_target=packed,
+                                             workspace=ws["dvl"], out=dvl)
+        specv.spec_kv_map(pages, ctx, off, budget, seats=seats, block_table=bt, out=kv_out, workspace=ws["kv"])
+        rules = dict(seats=seats, draft_tokens=d["tokens"], verify_len=vl, mask=ok_d, mask_rows=mask_rows,
+                     workspace=ws["rules"])
+        specv.spec_logit_rules(packed, h, target_row_off=off, **rules)
+        specv.spec_logit_rules(d["draft"], h, out=draft, **rules)
+        acc, out = specv.spec_verify_mixture(packed, draft, d["mix_w"], d["tokens"], d["u"], d["g"], 1.1, verify_len=vl,
+                                             target_row_off=off[:B], workspace=ws["ver"], out=ver)
+        specv.spec_history_add(h, out, seats=seats, workspace=ws["rules"])
+        torch.add(ctx, acc, out=keep)
+        keep.add_(1)
+        specv.spec_kv_release(pages, seats, keep_len=keep, workspace=ws["kv"])
+        ctx.copy_(keep)
+
+    counts, seen = h.counts.cpu().numpy().copy(), h.seen.cpu().numpy().view(np.uint32).copy()
+    params = dict(repetition=h.repetition.cpu().numpy(), frequency=h.frequency.cpu().numpy(),
+                  presence=h.presence.cpu().numpy(), bias_tokens=h.bias_tokens.cpu().numpy(),
+                  bias_values=h.bias_values.cpu().numpy())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    captured, flags = None, 0
+    with torch.cuda.stream(s):
+        if graph:
+            captured = torch.cuda.CUDAGraph()
+            s.synchronize()
+            with torch.cuda.graph(captured, stream=s):
+                step()
+        for trial in range(4):
+            scores = -np.sort(-g.beta(5, 2, (B, L)), axis=1).astype(np.float32)
+            u, toks = g.random((B, L), dtype=np.float32), x.tokens.copy()
+            if trial % 2:
+                toks[:, 1] = toks[:, 0]                       # a drafted token twice in a block
+            d["scores"].copy_(dev(scores))
+            d["u"].copy_(dev(u))
+            d["tokens"].copy_(dev(toks))
+            captured.replay() if graph else step()
+            s.synchronize()
+            ra = oracle.dvl_allocate(scores, budget)
+            vl, off = ra["verify_len"], ra["offsets"]
+            np.testing.assert_array_equal(dvl[1].cpu().numpy(), off)
+            # paging
+            r = model.map(ctx_h, off, budget, seats_h)
+            np.testing.assert_array_equal(kv_out[0].cpu().numpy(), r["slots"])
+            np.testing.assert_array_equal(kv_out[1].cpu().numpy(), r["positions"])
+            for b in range(B):
+                assert bt[b, :len(r["tables"][b])].tolist() == r["tables"][b]
+            # rules
+            common = dict(tokens=toks, verify_len=vl, seats=seats_h, counts=counts, seen=seen,
+                          mask=plain.pack_bits(ok), mask_rows=mask_rows.cpu().numpy(), **params)
+            dense = oracle.pack(x.target, vl, off, budget)
+            rt = plain.logit_rules(dense, B, 1, L + 1, L, row_off=off[:B], **common)
+            check_rows(host(packed), dense, rt, "bf16")
+            flat = x.draft.reshape(-1, V)
+            rd = plain.logit_rules(flat, B, K, L, L, **common)
+            got = host(draft).reshape(-1, V)
+            check_rows(got, flat, rd, "bf16", got)
+            # verification of the edited rows, then the state
+            ref = oracle.verify(host(packed), host(draft), toks, u, x.g, 1.1, mix_w=x.mix_w, verify_len=vl,
+                                target_row_off=off[:B], diag=True)
+            flags |= ref["flags"]
+            acc, out = ver[0].cpu().numpy(), ver[1].cpu().numpy()
+            check_verify(acc, out, ref, verify_len=vl)
+            counts, seen, _ = plain.history_add(counts, seen, seats_h, out, True)
+            np.testing.assert_array_equal(h.counts.cpu().numpy(), counts)
+            np.testing.assert_array_equal(h.seen.cpu().numpy().view(np.uint32), seen)
+            ctx_h = ctx_h + acc + 1
+            model.release(seats_h, ctx_h)
+            assert pages.free_pages[:int(pages.free_count)].tolist() == model.stack
+            np.testing.assert_array_equal(ctx.cpu().numpy(), ctx_h)
+    # a drafted token that the mask forbids has probability 0 on both sides: verification reports it, as the oracle does
+    assert {k: w.status() for k, w in ws.items()} == dict(dvl=0, ver=flags, rules=0, kv=0)
+    del captured
+
+
+def test_calls_on_two_streams_share_a_rules_workspace():
+    """Two calls at once on their own rows, one history, one workspace: it holds the status word alone."""
+    a, b = Case(41, 4, 1, 3, 20000, rows=4, bias=8), Case(42, 4, 1, 3, 20000, rows=4, bias=8)
+    ws = specv.Workspace(256)
+    xs = [logits_to_torch(c.x).view(4, 1, 4, 20000) for c in (a, b)]
+    args = [dict(seats=dev(c.seats), draft_tokens=dev(c.tokens), verify_len=dev(c.vlen)) for c in (a, b)]
+    hs = [c.history() for c in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s, x, h, k in zip(streams, xs, hs, args):
+        with torch.cuda.stream(s):
+            specv.spec_logit_rules(x, h, workspace=ws, **k)
+    torch.cuda.synchronize()
+    for c, x in zip((a, b), xs):
+        check_rows(host(x).reshape(c.x.shape), c.x, c.oracle(), "bf16")
+    assert ws.status() == 0
