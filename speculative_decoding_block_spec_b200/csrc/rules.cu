@@ -20,8 +20,10 @@
 
 namespace specv {
 
-constexpr int kRange = 1024;          // tokens of one warp: 32 words of the bit tables, one per lane
-constexpr int kRangeWords = kRange / 32;
+constexpr int kTile = 32 * kThreads;   // tokens of one block: one word of the bit tables per thread
+constexpr int kWarpTile = 32 * 32;     // of one warp
+constexpr int kRowsMax = SPEC_MAX_K * (SPEC_MAX_L + 1);
+static_assert(SPEC_MAX_BIAS * 8 <= kTile * 2, "the bias list is staged in the token list's shared memory");
 
 template <int DT> __device__ __forceinline__ float load_x(const char* row, int64_t v);
 template <> __device__ __forceinline__ float load_x<0>(const char* row, int64_t v) {
@@ -45,196 +47,277 @@ template <int DT> __device__ __forceinline__ void copy_x(char* out, const char* 
   else reinterpret_cast<unsigned short*>(out)[v] = reinterpret_cast<const unsigned short*>(in)[v];
 }
 
-// One warp: 1024 tokens of up to `per` rows of one request. Warps own their
-// tokens alone, so nothing but __syncwarp orders the accesses.
+// The -inf pattern of 16 bytes of logits.
+template <int DT> __device__ __forceinline__ uint4 neg_inf16() {
+  const uint32_t w = DT == 0 ? 0xff800000u : 0xff80ff80u;
+  return make_uint4(w, w, w, w);
+}
+
+// One warp's 1024 tokens of one row: out of place the copy, and -inf where the
+// mask forbids. `allow` and `skip` are the lane's words of the mask and of the
+// tokens that another block writes (out of place only). Whole 16-byte vectors
+// of the output's alignment, single elements at both ends.
+template <int DT, bool INPLACE>
+__device__ __forceinline__ void stream_row(const char* src, char* dst, int span, uint32_t allow, uint32_t skip) {
+  constexpr int es = Elem<DT>::kBytes, E = Elem<DT>::kPerVec;
+  const int lane = threadIdx.x & 31;
+  const bool vec = INPLACE || ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
+  const int head = vec ? min(span, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / es) : span;
+  const int nvec = (span - head) / E;
+  uint4 v[kWarpTile / E / 32];
+  if constexpr (!INPLACE) {
+#pragma unroll
+    for (int t = 0; t < kWarpTile / E / 32; ++t)
+      if (lane + 32 * t < nvec) v[t] = ldg16(src + (head + (lane + 32 * t) * E) * es);
+  }
+  skip &= allow;  // a forbidden token is -inf whoever owns it
+  const bool plain = __all_sync(0xffffffffu, allow == 0xffffffffu && skip == 0u);
+  if (INPLACE && plain) return;
+#pragma unroll
+  for (int t = 0; t < kWarpTile / E / 32; ++t) {
+    const int j = lane + 32 * t, o = min(head + j * E, kWarpTile - 1);
+    uint32_t ok = (1u << E) - 1u, no = 0u;
+    if (!plain) {  // bits o ... o + E - 1 of the warp's 32 words
+      const int w = o >> 5, w1 = min(w + 1, 31);
+      ok &= __funnelshift_r(__shfl_sync(0xffffffffu, allow, w), __shfl_sync(0xffffffffu, allow, w1), o & 31);
+      if constexpr (!INPLACE)
+        no = ((1u << E) - 1u) &
+             __funnelshift_r(__shfl_sync(0xffffffffu, skip, w), __shfl_sync(0xffffffffu, skip, w1), o & 31);
+    }
+    if (j >= nvec) continue;
+    char* at = dst + o * es;
+    if (ok == 0u) {
+      *reinterpret_cast<uint4*>(at) = neg_inf16<DT>();
+    } else if (ok == (1u << E) - 1u && no == 0u) {
+      if constexpr (!INPLACE) *reinterpret_cast<uint4*>(at) = v[t];
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (!(ok >> e & 1)) store_x<DT>(at, e, -INFINITY);
+        else if (!INPLACE && !(no >> e & 1)) copy_x<DT>(at, src + o * es, e);
+      }
+    }
+  }
+  // the elements before the first and behind the last vector
+  const int tail = head + nvec * E;
+  for (int k0 = 0; k0 < head + span - tail; k0 += 32) {
+    const int k = k0 + lane, o = k < head ? k : tail + k - head;
+    const bool in = o < span;
+    const int w = min(o, kWarpTile - 1) >> 5;
+    const uint32_t ok = __shfl_sync(0xffffffffu, allow, w), no = __shfl_sync(0xffffffffu, skip, w);
+    if (!in) continue;
+    if (!(ok >> (o & 31) & 1)) store_x<DT>(dst, o, -INFINITY);
+    else if (!INPLACE && !(no >> (o & 31) & 1)) copy_x<DT>(dst, src, o);
+  }
+}
+
+// Blocks (x, b, z): 8192 tokens of the vocabulary (or, behind those, 256
+// entries of the request's bias list) in rows q0 .. q1 of request b. A token
+// with a bias belongs to the bias block, every other one to its tile's block.
+//
+// A tile's block compacts its named tokens (seen or drafted) into a list in
+// shared memory and hands them to the threads, spare threads taking further
+// rows: the ids of real histories crowd in a few tiles, and the list spreads a
+// crowded tile over the whole block.
 template <int DT, bool INPLACE>
 __global__ void __launch_bounds__(kThreads) k_logit_rules(const RulesArgs a) {
-  extern __shared__ float s_bias_all[];  // [kWarps][kRange] when there are biases
-  __shared__ uint16_t s_list_all[kWarps][kRange];
-  __shared__ uint32_t s_seen_all[kWarps][32], s_draft_all[kWarps][32], s_bset_all[kWarps][32];
-  __shared__ int s_tok_all[kWarps][32];
+  __shared__ __align__(16) uint16_t s_list[kTile];
+  __shared__ uint32_t s_draft[kThreads], s_excl[kThreads];
+  __shared__ int s_tok[32];
+  __shared__ int64_t s_row[kRowsMax];
+  __shared__ int16_t s_pos[kRowsMax];
+  __shared__ int s_n;
+  constexpr int es = Elem<DT>::kBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.y;
+  const int64_t V = a.V, W = (V + 31) / 32;
+  const int tiles = static_cast<int>((V + kTile - 1) / kTile);
+  const bool bias_block = static_cast<int>(blockIdx.x) >= tiles;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTile, w0 = t0 / 32;
+  const bool first = blockIdx.z == 0 && blockIdx.x == 0;
+  s_draft[tid] = s_excl[tid] = 0u;
+  if (tid < 32) s_tok[tid] = -1;
+  if (tid == 0) s_n = 0;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRange;
-  const int64_t V = a.V;
-  if (t0 >= V) return;
-  const int span = static_cast<int>(min(static_cast<int64_t>(kRange), V - t0));
-  const int b = blockIdx.y;
-  const int64_t W = (V + 31) / 32, w0 = t0 / 32;
-  const bool first = t0 == 0 && blockIdx.z == 0 && lane == 0;
 
   // the request: a value outside its range leaves all its rows as they were
-  int flag = 0;
   const int ell = a.vlen ? a.vlen[b] : a.L;
-  if (ell < 0 || ell > a.L) flag |= kFlagVerifyLen;
-  const int nrow = ell + a.rows - a.L;
-  int64_t row0 = 0;
-  if (a.row_off) {
-    row0 = a.row_off[b];
-    if (!flag && (row0 < 0 || row0 + nrow > a.n_rows)) flag |= kFlagIndex;
-  }
-  int seat = -1;
-  if (a.h.counts) {
-    seat = a.seats ? a.seats[b] : b;
-    if (seat >= a.h.seats) flag |= kFlagIndex;
-  }
+  const int64_t row0 = a.row_off ? a.row_off[b] : 0;
+  const int seat = a.h.counts ? (a.seats ? a.seats[b] : b) : -1;
+  const int m = a.mask ? (a.mask_rows ? a.mask_rows[b] : b) : -1;
+  const bool sat = seat >= 0 && seat < a.h.seats;
   float rep = 1.f, freq = 0.f, pres = 0.f;
-  if (seat >= 0 && seat < a.h.seats) {
+  uint32_t seen = 0u;
+  if (sat) {
     if (a.h.repetition) rep = a.h.repetition[seat];
     if (a.h.frequency) freq = a.h.frequency[seat];
     if (a.h.presence) pres = a.h.presence[seat];
-    if (!(rep > 0.f && rep < INFINITY && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY)) flag |= kFlagParam;
+    if (!bias_block && w0 + tid < W) seen = a.h.seen[seat * W + w0 + tid];
   }
-  int m = -1;
-  if (a.mask) {
-    m = a.mask_rows ? a.mask_rows[b] : b;
-    if (m >= a.n_masks) flag |= kFlagIndex;
-  }
+  const int nrow = ell + a.rows - a.L;
+  int flag = 0;
+  if (ell < 0 || ell > a.L) flag |= kFlagVerifyLen;
+  else if (a.row_off && (row0 < 0 || row0 + nrow > a.n_rows)) flag |= kFlagIndex;
+  if ((a.h.counts && seat >= a.h.seats) || (a.mask && m >= a.n_masks)) flag |= kFlagIndex;
+  if (!(rep > 0.f && rep < INFINITY && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY)) flag |= kFlagParam;
   if (flag) {
-    if (first) atomicOr(a.status, flag);
+    if (first && tid == 0) atomicOr(a.status, flag);
     return;
   }
-  const int total = a.K * nrow;
-  const int q0 = blockIdx.z * a.per, q1 = min(total, q0 + a.per);
-  const bool pen = seat >= 0 && (rep != 1.f || freq != 0.f || pres != 0.f);
-  const bool bias = seat >= 0 && a.h.n_bias > 0;
-  const int64_t es = Elem<DT>::kBytes;
-  auto row_of = [&](int z, int i) -> int64_t {
-    return a.row_off ? row0 + i : (static_cast<int64_t>(b) * a.K + z) * a.rows + i;
+  const bool pen = sat && (rep != 1.f || freq != 0.f || pres != 0.f);
+  const int n_bias = sat ? a.h.n_bias : 0;
+  const int q0 = blockIdx.z * a.per, q1 = min(a.K * nrow, q0 + a.per), nq = q1 - q0;
+  if (pen && first && tid < ell) {
+    const int x = a.tokens[static_cast<int64_t>(b) * a.L + tid];
+    if (x < 0 || x >= V) atomicOr(a.status, kFlagTokenRange);
+  }
+  if (nq <= 0 || (INPLACE && !pen && m < 0 && !bias_block)) return;
+  for (int q = tid; q < nq; q += kThreads) {
+    const int z = (q0 + q) / nrow, i = q0 + q - z * nrow;
+    s_row[q] = a.row_off ? row0 + i : (static_cast<int64_t>(b) * a.K + z) * a.rows + i;
+    s_pos[q] = static_cast<int16_t>(i);
+  }
+  const uint32_t* mask = a.mask + (m >= 0 ? static_cast<int64_t>(m) * a.mask_len * W : 0);
+
+  // the value of token v (named, known to the rules by count0 / add / drafted) in row q, and whether it changes
+  auto edit = [&](float x, bool was_seen, int count0, uint32_t drafted, float add, int i) -> float {
+    const int extra = __popc(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
+    const int c = count0 + extra;
+    float y = was_seen || extra > 0 ? (x > 0.f ? x / rep : x * rep) : x;
+    return y - freq * static_cast<float>(c) - (c > 0 ? pres : 0.f) + add;
+  };
+  // all rows of one token for the threads sub, sub + groups, ...: four rows' loads in flight
+  auto rows_of = [&](int64_t v, int sub, int groups, bool was_seen, uint32_t drafted, float add, bool biased) {
+    const int count0 = was_seen ? a.h.counts[seat * V + v] : 0;
+    const uint32_t bit = 1u << (v & 31);
+    for (int q = sub; q < nq; q += 4 * groups) {
+      float x[4];
+      bool on[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = q + k * groups;
+        on[k] = r < nq;
+        if (!on[k]) continue;
+        const int i = s_pos[r];
+        if (!was_seen && !biased && !(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u))) on[k] = false;
+        else if (m >= 0) on[k] = mask[i * W + (v >> 5)] & bit;
+        if (on[k]) x[k] = load_x<DT>(a.x + s_row[r] * V * es, v);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (on[k]) store_x<DT>(a.out + s_row[q + k * groups] * V * es, v,
+                               edit(x[k], was_seen, count0, drafted, add, s_pos[q + k * groups]));
+    }
+  };
+  auto drafted_of = [&](int64_t v) -> uint32_t {
+    uint32_t d = 0;
+    for (int k = 0; k < ell; ++k) d |= (s_tok[k] == v ? 1u : 0u) << k;
+    return d;
   };
 
-  // the named tokens of this range: seen bits, drafted tokens, biased tokens
-  uint32_t* s_seen = s_seen_all[warp];
-  uint32_t* s_draft = s_draft_all[warp];
-  uint32_t* s_bset = s_bset_all[warp];
-  int* s_tok = s_tok_all[warp];
-  uint16_t* list = s_list_all[warp];
-  float* s_bias = s_bias_all + warp * kRange;
-  const bool in = w0 + lane < W;
-  s_seen[lane] = pen && in ? a.h.seen[seat * W + w0 + lane] : 0u;
-  s_draft[lane] = 0u;
-  s_bset[lane] = 0u;
-  s_tok[lane] = -1;
-  __syncwarp();
-  if (pen && lane < a.L) {
-    const int64_t x = a.tokens[static_cast<int64_t>(b) * a.L + lane];
-    if (x < 0 || x >= V) {
-      if (t0 == 0 && blockIdx.z == 0) atomicOr(a.status, kFlagTokenRange);
-    } else if (x >= t0 && x < t0 + kRange) {
-      s_tok[lane] = static_cast<int>(x - t0);
+  if (bias_block) {
+    int* tok = reinterpret_cast<int*>(s_list);
+    float* val = reinterpret_cast<float*>(s_list) + SPEC_MAX_BIAS;
+    for (int e = tid; e < n_bias; e += kThreads) {
+      tok[e] = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e];
+      val[e] = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e];
+      if (tok[e] >= V && blockIdx.z == 0) atomicOr(a.status, kFlagTokenRange);
+    }
+    if (pen && tid < ell) s_tok[tid] = a.tokens[static_cast<int64_t>(b) * a.L + tid];
+    __syncthreads();
+    const int e0 = (static_cast<int>(blockIdx.x) - tiles) * kThreads;
+    const int take = min(kThreads, n_bias - e0);
+    if (take <= 0) return;
+    const int groups = kThreads / take, sub = tid / take, e = e0 + tid - sub * take;
+    if (sub >= groups) return;
+    const int v = tok[e];
+    if (v < 0 || v >= V) return;
+    // the first entry of a token speaks for all of them and adds them up in list order
+    float add = 0.f;
+    for (int k = 0; k < n_bias; ++k) {
+      if (tok[k] != v) continue;
+      if (k < e) return;
+      add += val[k];
+    }
+    const bool was_seen = pen && (a.h.seen[seat * W + (v >> 5)] >> (v & 31) & 1);
+    rows_of(v, sub, groups, was_seen, pen ? drafted_of(v) : 0u, add, true);
+    return;
+  }
+
+  const int span = static_cast<int>(min(static_cast<int64_t>(kTile), V - t0));
+  __syncthreads();
+  if (pen && tid < ell) {  // the drafted tokens that a processed row can hold
+    const int64_t x = a.tokens[static_cast<int64_t>(b) * a.L + tid];
+    if (x >= t0 && x < t0 + span) {
+      s_tok[tid] = static_cast<int>(x);
       atomicOr(&s_draft[(x - t0) >> 5], 1u << (x & 31));
     }
   }
-  if (q0 >= q1) return;
-  if (bias) {
-    const int32_t* bt = a.h.bias_tokens + static_cast<int64_t>(seat) * a.h.n_bias;
-    const float* bv = a.h.bias_values + static_cast<int64_t>(seat) * a.h.n_bias;
-    for (int e0 = 0; e0 < a.h.n_bias; e0 += 32) {
-      const int e = e0 + lane;
-      const int64_t x = e < a.h.n_bias ? bt[e] : -1;
-      if (x >= V && t0 == 0 && blockIdx.z == 0) atomicOr(a.status, kFlagTokenRange);
-      const bool hit = x >= t0 && x < t0 + span;
-      const float val = hit ? bv[e] : 0.f;
-      // entries of one token add up in list order, whatever lane holds them
-      for (uint32_t left = __ballot_sync(0xffffffffu, hit); left; left &= left - 1) {
-        const int src = __ffs(left) - 1;
-        const int at = __shfl_sync(0xffffffffu, static_cast<int>(x - t0), src);
-        const float add = __shfl_sync(0xffffffffu, val, src);
-        if (lane == 0) {
-          const uint32_t bit = 1u << (at & 31);
-          const bool had = s_bset[at >> 5] & bit;
-          s_bias[at] = had ? s_bias[at] + add : add;
-          s_bset[at >> 5] |= bit;
-        }
-        __syncwarp();
-      }
-    }
+  for (int e = tid; e < n_bias; e += kThreads) {
+    const int64_t x = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e];
+    if (x >= t0 && x < t0 + span) atomicOr(&s_excl[(x - t0) >> 5], 1u << (x & 31));
   }
-  __syncwarp();
-  uint32_t word = s_seen[lane] | s_draft[lane] | s_bset[lane];
-  if (lane * 32 + 32 > span) word &= lane * 32 >= span ? 0u : (1u << (span - lane * 32)) - 1u;
-  int incl = __popc(word);
+  __syncthreads();
+  if (pen) {
+    uint32_t word = (seen | s_draft[tid]) & ~s_excl[tid];
+    if (tid * 32 + 32 > span) word &= tid * 32 >= span ? 0u : (1u << (span - tid * 32)) - 1u;
+    const int mine = __popc(word);
+    int incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    int at = 0;
+    if (lane == 31) at = atomicAdd(&s_n, incl);  // the warps' order in the list is free: tokens are independent
+    at = __shfl_sync(0xffffffffu, at, 31) + incl - mine;
+    for (uint32_t left = word; left; left &= left - 1)
+      s_list[at++] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
   }
-  const int n = __shfl_sync(0xffffffffu, incl, 31);
-  for (int at = incl - __popc(word); word; word &= word - 1)
-    list[at++] = static_cast<uint16_t>(lane * 32 + __ffs(word) - 1);
-  __syncwarp();
-
-  // rows: the mask's -inf (and the copy, out of place)
+  // seen bits of the list's tokens, for the threads that take them
+  const uint32_t excl = s_excl[tid];
+  __syncthreads();
+  s_excl[tid] = seen;
   if (!INPLACE || m >= 0) {
-    for (int q = q0; q < q1; ++q) {
-      const int z = q / nrow, i = q - z * nrow;
-      const int64_t r = row_of(z, i);
-      const char* src = a.x + (r * V + t0) * es;
-      char* dst = a.out + (r * V + t0) * es;
-      uint32_t allow = 0xffffffffu;
-      if (m >= 0 && in) allow = a.mask[(static_cast<int64_t>(m) * a.mask_len + i) * W + w0 + lane];
-      for (int w = 0; w < kRangeWords; ++w) {
-        const uint32_t ok = __shfl_sync(0xffffffffu, allow, w);
-        const int v = w * 32 + lane;
-        if (v < span) {
-          if (!(ok >> lane & 1)) store_x<DT>(dst, v, -INFINITY);
-          else if (!INPLACE) copy_x<DT>(dst, src, v);
-        }
+    const int wspan = min(kWarpTile, span - warp * kWarpTile);
+    if (wspan > 0) {
+      const int64_t at = t0 + warp * kWarpTile;
+      for (int q = 0; q < nq; ++q) {
+        uint32_t allow = 0xffffffffu;
+        if (m >= 0 && w0 + tid < W) allow = mask[s_pos[q] * W + w0 + tid];
+        const int64_t off = (s_row[q] * V + at) * es;
+        stream_row<DT, INPLACE>(a.x + off, a.out + off, wspan, allow, excl);
       }
     }
-    __syncwarp();
   }
-
-  // the named tokens: up to 32 at a time, the lanes that are left over take further rows
-  for (int e0 = 0; e0 < n; e0 += 32) {
-    const int take = min(32, n - e0);
-    const int groups = 32 / take;
-    const int sub = lane / take, e = e0 + lane - sub * take;
-    if (sub < groups) {
-      const int v = list[e];
-      const uint32_t bit = 1u << (v & 31);
-      const bool seen = s_seen[v >> 5] & bit;
-      const bool biased = s_bset[v >> 5] & bit;
-      const int count = seen ? a.h.counts[seat * V + t0 + v] : 0;
-      const float add = biased ? s_bias[v] : 0.f;
-      uint32_t drafted = 0;
-      if (s_draft[v >> 5] & bit)
-        for (int k = 0; k < a.L; ++k) drafted |= (s_tok[k] == v ? 1u : 0u) << k;
-      for (int q = q0 + sub; q < q1; q += groups) {
-        const int z = q / nrow, i = q - z * nrow;
-        const int extra = __popc(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
-        const bool known = seen || extra > 0;
-        if (!known && !biased) continue;
-        if (m >= 0 && !(a.mask[(static_cast<int64_t>(m) * a.mask_len + i) * W + w0 + (v >> 5)] & bit)) continue;
-        const int64_t r = row_of(z, i);
-        const float x = load_x<DT>(a.x + (r * V + t0) * es, v);
-        const int c = count + extra;
-        float y = known ? (x > 0.f ? x / rep : x * rep) : x;
-        y = y - freq * static_cast<float>(c) - (c > 0 ? pres : 0.f) + add;
-        store_x<DT>(a.out + (r * V + t0) * es, v, y);
-      }
-    }
-    __syncwarp();
+  __syncthreads();  // out of place: the copies come before the edits
+  const int n = s_n;
+  for (int e0 = 0; e0 < n; e0 += kThreads) {
+    const int take = min(kThreads, n - e0);
+    const int groups = kThreads / take, sub = tid / take;
+    if (sub >= groups) continue;
+    const int v = s_list[e0 + tid - sub * take];
+    const uint32_t bit = 1u << (v & 31);
+    rows_of(t0 + v, sub, groups, s_excl[v >> 5] & bit, s_draft[v >> 5] & bit ? drafted_of(t0 + v) : 0u, 0.f, false);
   }
 }
 
 cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st) {
   RulesArgs a = args;
-  const int64_t ranges = (a.V + kRange - 1) / kRange;
+  const int64_t tiles = (a.V + kTile - 1) / kTile;
+  const int n_bias = a.h.counts ? a.h.n_bias : 0;
+  const int64_t x = tiles + (n_bias + kThreads - 1) / kThreads;
   const int most = a.K * a.rows;
-  a.per = 4;
-  const dim3 grid(static_cast<unsigned>((ranges + kWarps - 1) / kWarps), static_cast<unsigned>(a.B),
-                  static_cast<unsigned>((most + a.per - 1) / a.per));
-  const size_t smem = a.h.counts && a.h.n_bias > 0 ? sizeof(float) * kRange * kWarps : 0;
+  // Rows are split over blocks until the grid fills the GPU twice (148 SMs of 8 blocks).
+  const int64_t want = 148 * 16;
+  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, want / (x * a.B))));
+  a.per = (most + z - 1) / z;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));
   const bool inplace = a.x == a.out;
   void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_logit_rules<0, true> : k_logit_rules<0, false>)
                                     : (inplace ? k_logit_rules<1, true> : k_logit_rules<1, false>);
-  if (smem) {  // with the static arrays above 48 KiB
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(k, grid, dim3(kThreads), smem, st, a);
+  return launch_pdl(k, grid, dim3(kThreads), 0, st, a);
 }
 
 // ------------------------------------------------------------------ history

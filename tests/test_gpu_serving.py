@@ -263,6 +263,19 @@ def test_rules_leave_out_what_they_cannot_do():
     run(lambda c: c.row_off.__setitem__(4, c.x.shape[0] - c.vlen[4]), specv.DEV_INDEX, packed=True)
 
 
+def test_rules_ignore_tokens_behind_the_verify_length():
+    """Drafted tokens at and past verify_len are not tested; what stands there is nobody's error."""
+    c = Case(17, 4, 1, 6, 900, rows=7, dtype="f32")
+    ref = c.oracle()
+    for b in range(4):
+        c.tokens[b, c.vlen[b]:] = [-1, 10 ** 6, 5, 2 ** 31 - 1, -7, 3][c.vlen[b]:]
+    ws = specv.Workspace(256)
+    x = logits_to_torch(c.x).view(4, 1, 7, 900)
+    c.call(x, workspace=ws)
+    check_rows(host(x).reshape(c.x.shape), c.x, ref, "f32")
+    assert ws.status() == 0
+
+
 def test_rules_neutral_call_writes_nothing():
     c = Case(5, 2, 1, 2, 500, rows=3, dtype="bf16")
     c.kw["repetition"][:], c.kw["frequency"][:], c.kw["presence"][:] = 1, 0, 0
