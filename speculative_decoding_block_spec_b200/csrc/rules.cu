@@ -20,10 +20,9 @@
 
 namespace specv {
 
-constexpr int kTile = 32 * kThreads;   // tokens of one block: one word of the bit tables per thread
-constexpr int kWarpTile = 32 * 32;     // of one warp
+constexpr int kChunk = 1024;  // tokens of one warp's step over a row: 32 words of a bit table
+constexpr int kListMax = 4096;
 constexpr int kRowsMax = SPEC_MAX_K * (SPEC_MAX_L + 1);
-static_assert(SPEC_MAX_BIAS * 8 <= kTile * 2, "the bias list is staged in the token list's shared memory");
 
 template <int DT> __device__ __forceinline__ float load_x(const char* row, int64_t v);
 template <> __device__ __forceinline__ float load_x<0>(const char* row, int64_t v) {
@@ -53,91 +52,121 @@ template <int DT> __device__ __forceinline__ uint4 neg_inf16() {
   return make_uint4(w, w, w, w);
 }
 
-// One warp's 1024 tokens of one row: out of place the copy, and -inf where the
-// mask forbids. `allow` and `skip` are the lane's words of the mask and of the
-// tokens that another block writes (out of place only). Whole 16-byte vectors
-// of the output's alignment, single elements at both ends.
-template <int DT, bool INPLACE>
-__device__ __forceinline__ void stream_row(const char* src, char* dst, int span, uint32_t allow, uint32_t skip) {
-  constexpr int es = Elem<DT>::kBytes, E = Elem<DT>::kPerVec;
-  const int lane = threadIdx.x & 31;
-  const bool vec = INPLACE || ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
-  const int head = vec ? min(span, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / es) : span;
-  const int nvec = (span - head) / E;
-  uint4 v[kWarpTile / E / 32];
-  if constexpr (!INPLACE) {
-#pragma unroll
-    for (int t = 0; t < kWarpTile / E / 32; ++t)
-      if (lane + 32 * t < nvec) v[t] = ldg16(src + (head + (lane + 32 * t) * E) * es);
-  }
-  skip &= allow;  // a forbidden token is -inf whoever owns it
-  const bool plain = __all_sync(0xffffffffu, allow == 0xffffffffu && skip == 0u);
-  if (INPLACE && plain) return;
-#pragma unroll
-  for (int t = 0; t < kWarpTile / E / 32; ++t) {
-    const int j = lane + 32 * t, o = min(head + j * E, kWarpTile - 1);
-    uint32_t ok = (1u << E) - 1u, no = 0u;
-    if (!plain) {  // bits o ... o + E - 1 of the warp's 32 words
-      const int w = o >> 5, w1 = min(w + 1, 31);
-      ok &= __funnelshift_r(__shfl_sync(0xffffffffu, allow, w), __shfl_sync(0xffffffffu, allow, w1), o & 31);
-      if constexpr (!INPLACE)
-        no = ((1u << E) - 1u) &
-             __funnelshift_r(__shfl_sync(0xffffffffu, skip, w), __shfl_sync(0xffffffffu, skip, w1), o & 31);
-    }
-    if (j >= nvec) continue;
-    char* at = dst + o * es;
-    if (ok == 0u) {
-      *reinterpret_cast<uint4*>(at) = neg_inf16<DT>();
-    } else if (ok == (1u << E) - 1u && no == 0u) {
-      if constexpr (!INPLACE) *reinterpret_cast<uint4*>(at) = v[t];
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (!(ok >> e & 1)) store_x<DT>(at, e, -INFINITY);
-        else if (!INPLACE && !(no >> e & 1)) copy_x<DT>(at, src + o * es, e);
-      }
-    }
-  }
-  // the elements before the first and behind the last vector
-  const int tail = head + nvec * E;
-  for (int k0 = 0; k0 < head + span - tail; k0 += 32) {
-    const int k = k0 + lane, o = k < head ? k : tail + k - head;
-    const bool in = o < span;
-    const int w = min(o, kWarpTile - 1) >> 5;
-    const uint32_t ok = __shfl_sync(0xffffffffu, allow, w), no = __shfl_sync(0xffffffffu, skip, w);
-    if (!in) continue;
-    if (!(ok >> (o & 31) & 1)) store_x<DT>(dst, o, -INFINITY);
-    else if (!INPLACE && !(no >> (o & 31) & 1)) copy_x<DT>(dst, src, o);
+// Words of `allow` whose groups of E bits are all 0 keep those bits: the
+// 16-byte vectors that are forbidden as a whole.
+template <int E> __device__ __forceinline__ uint32_t whole_groups(uint32_t forbid) {
+  uint32_t t = forbid & (forbid >> 1);
+  t &= t >> 2;
+  if (E == 8) t &= t >> 4;
+  return t & (E == 8 ? 0x01010101u : 0x11111111u);
+}
+
+// bf16 pairs / fp32 words of a vector where the mask allows them, -inf elsewhere.
+template <int DT> __device__ __forceinline__ uint4 choose(const uint4& v, uint32_t ok) {
+  const uint4 f = neg_inf16<DT>();
+  if constexpr (DT == 0) {
+    return make_uint4(ok & 1 ? v.x : f.x, ok & 2 ? v.y : f.y, ok & 4 ? v.z : f.z, ok & 8 ? v.w : f.w);
+  } else {
+    auto pick = [&](uint32_t x, uint32_t b) {
+      const uint32_t keep = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
+      return (x & keep) | (0xff80ff80u & ~keep);
+    };
+    return make_uint4(pick(v.x, ok), pick(v.y, ok >> 2), pick(v.z, ok >> 4), pick(v.w, ok >> 6));
   }
 }
 
-// Blocks (x, b, z): 8192 tokens of the vocabulary (or, behind those, 256
-// entries of the request's bias list) in rows q0 .. q1 of request b. A token
-// with a bias belongs to the bias block, every other one to its tile's block.
-//
-// A tile's block compacts its named tokens (seen or drafted) into a list in
-// shared memory and hands them to the threads, spare threads taking further
-// rows: the ids of real histories crowd in a few tiles, and the list spreads a
-// crowded tile over the whole block.
+// One warp's 1024 tokens of one row: -inf where the mask forbids and, out of
+// place, the copy. `allow`: the lane's 32 tokens of the mask. 16-byte vectors
+// at the output's alignment (the mask is shifted to it), elements at the ends;
+// in place, vectors that are forbidden only in part are written by elements.
 template <int DT, bool INPLACE>
-__global__ void __launch_bounds__(kThreads) k_logit_rules(const RulesArgs a) {
-  __shared__ __align__(16) uint16_t s_list[kTile];
-  __shared__ uint32_t s_draft[kThreads], s_excl[kThreads];
-  __shared__ int s_tok[32];
-  __shared__ int64_t s_row[kRowsMax];
-  __shared__ int16_t s_pos[kRowsMax];
-  __shared__ int s_n;
+__device__ __forceinline__ void stream_chunk(const char* src, char* dst, int span, uint32_t allow) {
+  constexpr int es = Elem<DT>::kBytes, E = Elem<DT>::kPerVec, NV = kChunk / E / 32;
+  const int lane = threadIdx.x & 31;
+  const bool vec = INPLACE || ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
+  if (!vec) {
+    for (int w = 0; w < 32; ++w) {
+      const uint32_t ok = __shfl_sync(0xffffffffu, allow, w);
+      const int o = w * 32 + lane;
+      if (o >= span) continue;
+      if (ok >> lane & 1) copy_x<DT>(dst, src, o);
+      else store_x<DT>(dst, o, -INFINITY);
+    }
+    return;
+  }
+  const int head = min(span, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / es);
+  const int nvec = (span - head) / E;
+  uint4 v[INPLACE ? 1 : NV];
+  if constexpr (!INPLACE) {
+#pragma unroll
+    for (int t = 0; t < NV; ++t)
+      if (lane + 32 * t < nvec) v[t] = ldg16(src + (head + (lane + 32 * t) * E) * es);
+  }
+  uint32_t ok = allow;  // bit i: token head + 32 lane + i
+  const uint32_t ends = __shfl_sync(0xffffffffu, allow, 0);
+  if (head) {
+    const uint32_t next = __shfl_down_sync(0xffffffffu, allow, 1);
+    ok = __funnelshift_r(ok, lane == 31 ? 0xffffffffu : next, head);
+  }
+  const int left = span - head - 32 * lane;
+  if (left < 32) ok |= left <= 0 ? 0xffffffffu : 0xffffffffu << left;
+  const int from = lane / (32 / E), at = lane % (32 / E) * E;  // vector lane + 32 t: bits `at` of lane from + t * E
+  if constexpr (INPLACE) {
+    const uint32_t whole = whole_groups<E>(~ok);
+    if (__any_sync(0xffffffffu, whole)) {
+#pragma unroll
+      for (int t = 0; t < NV; ++t)
+        if (__shfl_sync(0xffffffffu, whole, from + t * E) >> at & 1)
+          *reinterpret_cast<uint4*>(dst + (head + (lane + 32 * t) * E) * es) = neg_inf16<DT>();
+    }
+    for (uint32_t part = ~ok & ~(whole * ((1u << E) - 1u)); part; part &= part - 1)
+      store_x<DT>(dst, head + 32 * lane + __ffs(part) - 1, -INFINITY);
+    if (lane < head && !(ends >> lane & 1)) store_x<DT>(dst, lane, -INFINITY);
+  } else {
+    const bool plain = __all_sync(0xffffffffu, ok == 0xffffffffu);
+#pragma unroll
+    for (int t = 0; t < NV; ++t) {
+      uint4 y = v[t];
+      if (!plain) y = choose<DT>(y, __shfl_sync(0xffffffffu, ok, from + t * E) >> at);
+      if (lane + 32 * t < nvec) *reinterpret_cast<uint4*>(dst + (head + (lane + 32 * t) * E) * es) = y;
+    }
+    const int tail = head + nvec * E, o = lane < head ? lane : tail + lane - head;  // fewer than 2 E <= 32 elements
+    const int w = min(o, kChunk - 1) >> 5;
+    const uint32_t mine = __shfl_sync(0xffffffffu, allow, w);
+    if (o < span && (lane < head || o >= tail)) {
+      if (mine >> (o & 31) & 1) copy_x<DT>(dst, src, o);
+      else store_x<DT>(dst, o, -INFINITY);
+    }
+  }
+}
+
+// Block (x, b, z): WPT * 8192 tokens of the vocabulary in rows q0 .. q1 of
+// request b.
+//
+// The ids of real histories crowd in the low end of the vocabulary. A block
+// therefore compacts its seen tokens into a list in shared memory and hands
+// them to its threads, spare threads taking further rows; a crowded tile is
+// spread over the whole block, and over further blocks by rows. Tokens that
+// are drafted or biased are taken out of the list and go a slower way.
+template <int DT, bool INPLACE, int WPT>
+__global__ void __launch_bounds__(kThreads, 6) k_logit_rules(const RulesArgs a) {
+  constexpr int kTile = WPT * 32 * kThreads;
   constexpr int es = Elem<DT>::kBytes;
+  __shared__ uint32_t s_word[WPT * kThreads];
+  __shared__ uint16_t s_list[kListMax];
+  __shared__ int64_t s_off[kRowsMax];  // first byte of a row
+  __shared__ int16_t s_pos[kRowsMax];
+  __shared__ int s_tok[32 + SPEC_MAX_BIAS];  // drafted tokens, then the bias list
+  __shared__ float s_val[SPEC_MAX_BIAS];
+  __shared__ uint16_t s_special[32 + SPEC_MAX_BIAS];
+  __shared__ int s_n, s_ns;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y;
   const int64_t V = a.V, W = (V + 31) / 32;
-  const int tiles = static_cast<int>((V + kTile - 1) / kTile);
-  const bool bias_block = static_cast<int>(blockIdx.x) >= tiles;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTile, w0 = t0 / 32;
+  const int span = static_cast<int>(min(static_cast<int64_t>(kTile), V - t0));
   const bool first = blockIdx.z == 0 && blockIdx.x == 0;
-  s_draft[tid] = s_excl[tid] = 0u;
-  if (tid < 32) s_tok[tid] = -1;
-  if (tid == 0) s_n = 0;
+  if (tid == 0) s_n = s_ns = 0;
   pdl_wait();
   pdl_trigger();
 
@@ -148,12 +177,17 @@ __global__ void __launch_bounds__(kThreads) k_logit_rules(const RulesArgs a) {
   const int m = a.mask ? (a.mask_rows ? a.mask_rows[b] : b) : -1;
   const bool sat = seat >= 0 && seat < a.h.seats;
   float rep = 1.f, freq = 0.f, pres = 0.f;
-  uint32_t seen = 0u;
+  uint32_t word[WPT];  // words tid, tid + 256, ... of the tile
+#pragma unroll
+  for (int k = 0; k < WPT; ++k) word[k] = 0u;
   if (sat) {
     if (a.h.repetition) rep = a.h.repetition[seat];
     if (a.h.frequency) freq = a.h.frequency[seat];
     if (a.h.presence) pres = a.h.presence[seat];
-    if (!bias_block && w0 + tid < W) seen = a.h.seen[seat * W + w0 + tid];
+    const uint32_t* seen = a.h.seen + seat * W + w0;
+#pragma unroll
+    for (int k = 0; k < WPT; ++k)
+      if ((tid + k * kThreads) * 32 < span) word[k] = seen[tid + k * kThreads];
   }
   const int nrow = ell + a.rows - a.L;
   int flag = 0;
@@ -166,158 +200,171 @@ __global__ void __launch_bounds__(kThreads) k_logit_rules(const RulesArgs a) {
     return;
   }
   const bool pen = sat && (rep != 1.f || freq != 0.f || pres != 0.f);
-  const int n_bias = sat ? a.h.n_bias : 0;
-  const int q0 = blockIdx.z * a.per, q1 = min(a.K * nrow, q0 + a.per), nq = q1 - q0;
-  if (pen && first && tid < ell) {
+  const int n_bias = sat ? a.h.n_bias : 0, n_tok = pen ? ell : 0;
+  const int q0 = blockIdx.z * a.per, nq = min(a.K * nrow, q0 + a.per) - q0;
+  if (first && tid < n_tok) {
     const int x = a.tokens[static_cast<int64_t>(b) * a.L + tid];
     if (x < 0 || x >= V) atomicOr(a.status, kFlagTokenRange);
   }
-  if (nq <= 0 || (INPLACE && !pen && m < 0 && !bias_block)) return;
+  if (nq <= 0 || (INPLACE && !pen && m < 0 && n_bias == 0)) return;
   for (int q = tid; q < nq; q += kThreads) {
     const int z = (q0 + q) / nrow, i = q0 + q - z * nrow;
-    s_row[q] = a.row_off ? row0 + i : (static_cast<int64_t>(b) * a.K + z) * a.rows + i;
+    const int64_t r = a.row_off ? row0 + i : (static_cast<int64_t>(b) * a.K + z) * a.rows + i;
+    s_off[q] = r * V * es;
     s_pos[q] = static_cast<int16_t>(i);
   }
   const uint32_t* mask = a.mask + (m >= 0 ? static_cast<int64_t>(m) * a.mask_len * W : 0);
-
-  // the value of token v (named, known to the rules by count0 / add / drafted) in row q, and whether it changes
-  auto edit = [&](float x, bool was_seen, int count0, uint32_t drafted, float add, int i) -> float {
-    const int extra = __popc(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
-    const int c = count0 + extra;
-    float y = was_seen || extra > 0 ? (x > 0.f ? x / rep : x * rep) : x;
-    return y - freq * static_cast<float>(c) - (c > 0 ? pres : 0.f) + add;
-  };
-  // all rows of one token for the threads sub, sub + groups, ...: four rows' loads in flight
-  auto rows_of = [&](int64_t v, int sub, int groups, bool was_seen, uint32_t drafted, float add, bool biased) {
-    const int count0 = was_seen ? a.h.counts[seat * V + v] : 0;
-    const uint32_t bit = 1u << (v & 31);
-    for (int q = sub; q < nq; q += 4 * groups) {
-      float x[4];
-      bool on[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = q + k * groups;
-        on[k] = r < nq;
-        if (!on[k]) continue;
-        const int i = s_pos[r];
-        if (!was_seen && !biased && !(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u))) on[k] = false;
-        else if (m >= 0) on[k] = mask[i * W + (v >> 5)] & bit;
-        if (on[k]) x[k] = load_x<DT>(a.x + s_row[r] * V * es, v);
+  for (int k = 0; k < WPT; ++k) {
+    const int at = (tid + k * kThreads) * 32;
+    if (!pen) word[k] = 0u;
+    else if (at + 32 > span) word[k] &= at >= span ? 0u : (1u << (span - at)) - 1u;
+  }
+
+  // drafted and biased tokens of the tile: out of the list, into s_special
+  if (n_tok + n_bias > 0) {
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) s_word[tid + k * kThreads] = word[k];
+  }
+  __syncthreads();  // s_n, s_ns, s_off, s_pos, s_word
+  if (n_tok + n_bias > 0) {
+    for (int e = tid; e < 32 + n_bias; e += kThreads) {
+      int x = -1;
+      if (e >= 32) {
+        x = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
+        s_val[e - 32] = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
+        if (first && x >= V) atomicOr(a.status, kFlagTokenRange);
+      } else if (e < n_tok) {
+        x = a.tokens[static_cast<int64_t>(b) * a.L + e];
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (on[k]) store_x<DT>(a.out + s_row[q + k * groups] * V * es, v,
-                               edit(x[k], was_seen, count0, drafted, add, s_pos[q + k * groups]));
+      s_tok[e] = x;
+      if (x >= t0 && x < t0 + span) {
+        s_special[atomicAdd(&s_ns, 1)] = static_cast<uint16_t>(e);
+        atomicAnd(&s_word[(x - t0) >> 5], ~(1u << (x & 31)));
+      }
     }
-  };
-  auto drafted_of = [&](int64_t v) -> uint32_t {
-    uint32_t d = 0;
-    for (int k = 0; k < ell; ++k) d |= (s_tok[k] == v ? 1u : 0u) << k;
-    return d;
-  };
-
-  if (bias_block) {
-    int* tok = reinterpret_cast<int*>(s_list);
-    float* val = reinterpret_cast<float*>(s_list) + SPEC_MAX_BIAS;
-    for (int e = tid; e < n_bias; e += kThreads) {
-      tok[e] = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e];
-      val[e] = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e];
-      if (tok[e] >= V && blockIdx.z == 0) atomicOr(a.status, kFlagTokenRange);
-    }
-    if (pen && tid < ell) s_tok[tid] = a.tokens[static_cast<int64_t>(b) * a.L + tid];
     __syncthreads();
-    const int e0 = (static_cast<int>(blockIdx.x) - tiles) * kThreads;
-    const int take = min(kThreads, n_bias - e0);
-    if (take <= 0) return;
-    const int groups = kThreads / take, sub = tid / take, e = e0 + tid - sub * take;
-    if (sub >= groups) return;
-    const int v = tok[e];
-    if (v < 0 || v >= V) return;
-    // the first entry of a token speaks for all of them and adds them up in list order
-    float add = 0.f;
-    for (int k = 0; k < n_bias; ++k) {
-      if (tok[k] != v) continue;
-      if (k < e) return;
-      add += val[k];
-    }
-    const bool was_seen = pen && (a.h.seen[seat * W + (v >> 5)] >> (v & 31) & 1);
-    rows_of(v, sub, groups, was_seen, pen ? drafted_of(v) : 0u, add, true);
-    return;
-  }
-
-  const int span = static_cast<int>(min(static_cast<int64_t>(kTile), V - t0));
-  __syncthreads();
-  if (pen && tid < ell) {  // the drafted tokens that a processed row can hold
-    const int64_t x = a.tokens[static_cast<int64_t>(b) * a.L + tid];
-    if (x >= t0 && x < t0 + span) {
-      s_tok[tid] = static_cast<int>(x);
-      atomicOr(&s_draft[(x - t0) >> 5], 1u << (x & 31));
-    }
-  }
-  for (int e = tid; e < n_bias; e += kThreads) {
-    const int64_t x = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e];
-    if (x >= t0 && x < t0 + span) atomicOr(&s_excl[(x - t0) >> 5], 1u << (x & 31));
-  }
-  __syncthreads();
-  if (pen) {
-    uint32_t word = (seen | s_draft[tid]) & ~s_excl[tid];
-    if (tid * 32 + 32 > span) word &= tid * 32 >= span ? 0u : (1u << (span - tid * 32)) - 1u;
-    const int mine = __popc(word);
-    int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    int at = 0;
-    if (lane == 31) at = atomicAdd(&s_n, incl);  // the warps' order in the list is free: tokens are independent
-    at = __shfl_sync(0xffffffffu, at, 31) + incl - mine;
-    for (uint32_t left = word; left; left &= left - 1)
-      s_list[at++] = static_cast<uint16_t>(tid * 32 + __ffs(left) - 1);
+    for (int k = 0; k < WPT; ++k) word[k] = s_word[tid + k * kThreads];
   }
-  // seen bits of the list's tokens, for the threads that take them
-  const uint32_t excl = s_excl[tid];
-  __syncthreads();
-  s_excl[tid] = seen;
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < WPT; ++k) mine += __popc(word[k]);
+  int rank = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, rank, o);
+    if (lane >= o) rank += t;
+  }
+  int base = 0;
+  if (lane == 31 && rank) base = atomicAdd(&s_n, rank);  // the warps' order is free: tokens are independent
+  rank = __shfl_sync(0xffffffffu, base, 31) + rank - mine;
+
   if (!INPLACE || m >= 0) {
-    const int wspan = min(kWarpTile, span - warp * kWarpTile);
-    if (wspan > 0) {
-      const int64_t at = t0 + warp * kWarpTile;
+    for (int c = warp; c * kChunk < span; c += kWarps) {
+      const int wspan = min(kChunk, span - c * kChunk);
+      const int64_t w = w0 + c * 32 + lane;
       for (int q = 0; q < nq; ++q) {
-        uint32_t allow = 0xffffffffu;
-        if (m >= 0 && w0 + tid < W) allow = mask[s_pos[q] * W + w0 + tid];
-        const int64_t off = (s_row[q] * V + at) * es;
-        stream_row<DT, INPLACE>(a.x + off, a.out + off, wspan, allow, excl);
+        const uint32_t allow = m >= 0 && w < W ? mask[s_pos[q] * W + w] : 0xffffffffu;
+        const int64_t off = s_off[q] + (t0 + c * kChunk) * es;
+        stream_chunk<DT, INPLACE>(a.x + off, a.out + off, wspan, allow);
       }
     }
   }
-  __syncthreads();  // out of place: the copies come before the edits
+
+  // the list, in rounds of kListMax tokens (one, unless the history holds most of the vocabulary)
+  __syncthreads();  // s_n; out of place: the copies come before the edits
   const int n = s_n;
-  for (int e0 = 0; e0 < n; e0 += kThreads) {
-    const int take = min(kThreads, n - e0);
+  for (int l0 = 0; l0 < n; l0 += kListMax) {
+    if (l0) __syncthreads();
+    int at = rank - l0;
+#pragma unroll
+    for (int k = 0; k < WPT; ++k)
+      for (uint32_t left = word[k]; left; left &= left - 1, ++at)
+        if (at >= 0 && at < kListMax)
+          s_list[at] = static_cast<uint16_t>((tid + k * kThreads) * 32 + __ffs(left) - 1);
+    __syncthreads();
+    const int ln = min(kListMax, n - l0);
+    for (int e0 = 0; e0 < ln; e0 += kThreads) {
+      const int take = min(kThreads, ln - e0);
+      const int groups = kThreads / take, sub = tid / take;
+      if (sub >= groups) continue;
+      const int64_t v = t0 + s_list[e0 + tid - sub * take];
+      const int c = a.h.counts[seat * V + v];
+      const char* x = a.x + v * es;
+      char* y = a.out + v * es;
+      for (int q = sub; q < nq; q += 4 * groups) {  // four rows' loads in flight
+        float f[4];
+        bool on[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = q + k * groups;
+          on[k] = r < nq;
+          if (on[k] && m >= 0) on[k] = mask[s_pos[r] * W + (v >> 5)] >> (v & 31) & 1;
+          if (on[k]) f[k] = load_x<DT>(x + s_off[r], 0);
+        }
+        const float minus = freq * static_cast<float>(c) + (c > 0 ? pres : 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (on[k]) store_x<DT>(y + s_off[q + k * groups], 0, (f[k] > 0.f ? f[k] / rep : f[k] * rep) - minus);
+      }
+    }
+  }
+
+  // drafted and biased tokens: the first of the entries that name a token speaks for all, in list order
+  const int ns = s_ns;
+  for (int e0 = 0; e0 < ns; e0 += kThreads) {
+    const int take = min(kThreads, ns - e0);
     const int groups = kThreads / take, sub = tid / take;
     if (sub >= groups) continue;
-    const int v = s_list[e0 + tid - sub * take];
-    const uint32_t bit = 1u << (v & 31);
-    rows_of(t0 + v, sub, groups, s_excl[v >> 5] & bit, s_draft[v >> 5] & bit ? drafted_of(t0 + v) : 0u, 0.f, false);
+    const int self = s_special[e0 + tid - sub * take];
+    const int64_t v = s_tok[self];
+    uint32_t drafted = 0u;
+    bool mute = false;
+    for (int k = 0; k < n_tok; ++k)
+      if (s_tok[k] == v) {
+        drafted |= 1u << k;
+        mute |= k < self;
+      }
+    float add = 0.f;
+    for (int k = 0; k < n_bias && !mute; ++k)
+      if (s_tok[32 + k] == v) {
+        add += s_val[k];
+        mute = 32 + k < self;
+      }
+    if (mute) continue;
+    const bool seen = pen && (a.h.seen[seat * W + (v >> 5)] >> (v & 31) & 1);
+    const int count = seen ? a.h.counts[seat * V + v] : 0;
+    for (int q = sub; q < nq; q += groups) {
+      const int i = s_pos[q];
+      const int extra = __popc(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u)), c = count + extra;
+      const bool known = seen || extra > 0;
+      if (!known && add == 0.f) continue;
+      if (m >= 0 && !(mask[i * W + (v >> 5)] >> (v & 31) & 1)) continue;
+      const float f = load_x<DT>(a.x + s_off[q], v);
+      const float g = known ? (f > 0.f ? f / rep : f * rep) : f;
+      store_x<DT>(a.out + s_off[q], v, g - freq * static_cast<float>(c) - (c > 0 ? pres : 0.f) + add);
+    }
   }
 }
 
-cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st) {
-  RulesArgs a = args;
-  const int64_t tiles = (a.V + kTile - 1) / kTile;
-  const int n_bias = a.h.counts ? a.h.n_bias : 0;
-  const int64_t x = tiles + (n_bias + kThreads - 1) / kThreads;
+template <int WPT>
+cudaError_t launch_tiles(RulesArgs a, int dtype, cudaStream_t st) {
+  const int64_t x = (a.V + WPT * 32 * kThreads - 1) / (WPT * 32 * kThreads);
   const int most = a.K * a.rows;
-  // Rows are split over blocks until the grid fills the GPU twice (148 SMs of 8 blocks).
-  const int64_t want = 148 * 16;
+  const int64_t want = 148 * 12;  // two waves of 6 blocks on 148 SMs, by splitting rows
   const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, want / (x * a.B))));
   a.per = (most + z - 1) / z;
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));
   const bool inplace = a.x == a.out;
-  void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_logit_rules<0, true> : k_logit_rules<0, false>)
-                                    : (inplace ? k_logit_rules<1, true> : k_logit_rules<1, false>);
+  void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_logit_rules<0, true, WPT> : k_logit_rules<0, false, WPT>)
+                                    : (inplace ? k_logit_rules<1, true, WPT> : k_logit_rules<1, false, WPT>);
   return launch_pdl(k, grid, dim3(kThreads), 0, st, a);
+}
+
+cudaError_t launch_logit_rules(const RulesArgs& a, int dtype, cudaStream_t st) {
+  const bool streams = a.x != a.out || a.mask;
+  return streams ? launch_tiles<1>(a, dtype, st) : launch_tiles<4>(a, dtype, st);
 }
 
 // ------------------------------------------------------------------ history
