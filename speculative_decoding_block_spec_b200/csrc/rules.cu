@@ -20,8 +20,23 @@
 
 namespace specv {
 
+#ifndef MINB
+#define MINB 2
+#endif
+#ifndef SMINB
+#define SMINB 6
+#endif
+#ifndef SROWS
+#define SROWS 4
+#endif
+#ifndef WANT
+#define WANT 4
+#endif
 constexpr int kChunk = 1024;  // tokens of one warp's step over a row: 32 words of a bit table
-constexpr int kListMax = 4096;
+constexpr int kStreamRows = SROWS;
+constexpr int kEditThreads = 512;
+constexpr int kEditTile = 10 * 32 * kEditThreads;  // tokens of the edit kernel's tile: 163,840
+constexpr int kListMax = 4096;  // seen tokens that are taken at a time
 constexpr int kRowsMax = SPEC_MAX_K * (SPEC_MAX_L + 1);
 
 template <int DT> __device__ __forceinline__ float load_x(const char* row, int64_t v);
@@ -96,11 +111,14 @@ __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int spa
   }
   const int head = min(span, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / es);
   const int nvec = (span - head) / E;
-  uint4 v[INPLACE ? 1 : NV];
+  src += (head + lane * E) * es;  // the lane's first vector
+  dst += (head + lane * E) * es;
+  constexpr int kStep = 32 * 16, kFly = 4;  // vectors in flight per lane
+  uint4 v[kFly];
   if constexpr (!INPLACE) {
 #pragma unroll
-    for (int t = 0; t < NV; ++t)
-      if (lane + 32 * t < nvec) v[t] = ldg16(src + (head + (lane + 32 * t) * E) * es);
+    for (int t = 0; t < kFly; ++t)
+      if (lane + 32 * t < nvec) v[t] = ldg16(src + t * kStep);
   }
   uint32_t ok = allow;  // bit i: token head + 32 lane + i
   const uint32_t ends = __shfl_sync(0xffffffffu, allow, 0);
@@ -117,254 +135,359 @@ __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int spa
 #pragma unroll
       for (int t = 0; t < NV; ++t)
         if (__shfl_sync(0xffffffffu, whole, from + t * E) >> at & 1)
-          *reinterpret_cast<uint4*>(dst + (head + (lane + 32 * t) * E) * es) = neg_inf16<DT>();
+          *reinterpret_cast<uint4*>(dst + t * kStep) = neg_inf16<DT>();
     }
+    dst += 32 * lane * es - lane * 16;  // the lane's 32 tokens
     for (uint32_t part = ~ok & ~(whole * ((1u << E) - 1u)); part; part &= part - 1)
-      store_x<DT>(dst, head + 32 * lane + __ffs(part) - 1, -INFINITY);
-    if (lane < head && !(ends >> lane & 1)) store_x<DT>(dst, lane, -INFINITY);
+      store_x<DT>(dst, __ffs(part) - 1, -INFINITY);
+    if (lane < head && !(ends >> lane & 1)) store_x<DT>(dst, lane - head - 32 * lane, -INFINITY);
   } else {
     const bool plain = __all_sync(0xffffffffu, ok == 0xffffffffu);
 #pragma unroll
-    for (int t = 0; t < NV; ++t) {
-      uint4 y = v[t];
-      if (!plain) y = choose<DT>(y, __shfl_sync(0xffffffffu, ok, from + t * E) >> at);
-      if (lane + 32 * t < nvec) *reinterpret_cast<uint4*>(dst + (head + (lane + 32 * t) * E) * es) = y;
+    for (int t0 = 0; t0 < NV; t0 += kFly) {
+#pragma unroll
+      for (int t = 0; t < kFly; ++t) {
+        uint4 y = v[t];
+        if (!plain) y = choose<DT>(y, __shfl_sync(0xffffffffu, ok, from + (t0 + t) * E) >> at);
+        if (lane + 32 * (t0 + t) < nvec) *reinterpret_cast<uint4*>(dst + (t0 + t) * kStep) = y;
+        if (t0 + kFly < NV && lane + 32 * (t0 + kFly + t) < nvec) v[t] = ldg16(src + (t0 + kFly + t) * kStep);
+      }
     }
-    const int tail = head + nvec * E, o = lane < head ? lane : tail + lane - head;  // fewer than 2 E <= 32 elements
-    const int w = min(o, kChunk - 1) >> 5;
-    const uint32_t mine = __shfl_sync(0xffffffffu, allow, w);
-    if (o < span && (lane < head || o >= tail)) {
-      if (mine >> (o & 31) & 1) copy_x<DT>(dst, src, o);
-      else store_x<DT>(dst, o, -INFINITY);
+    // elements before the first and behind the last vector: fewer than 2 E <= 16, one to a lane
+    const int tail = head + nvec * E, o = lane < head ? lane : tail + lane - head;
+    const uint32_t mine = __shfl_sync(0xffffffffu, allow, min(o, kChunk - 1) >> 5);
+    if (o < span) {
+      const int rel = o - head - lane * E;
+      if (mine >> (o & 31) & 1) copy_x<DT>(dst, src, rel);
+      else store_x<DT>(dst, rel, -INFINITY);
     }
   }
 }
 
-// Block (x, b, z): WPT * 8192 tokens of the vocabulary in rows q0 .. q1 of
-// request b.
+// What a block needs to know of its request. A value outside its range leaves
+// all the request's rows as they were; `flag` says which it was.
+struct Request {
+  int nrow, ell, seat, m, flag;
+  int64_t row0;
+  float rep, freq, pres;
+  bool sat, pen;
+};
+__device__ __forceinline__ Request load_request(const RulesArgs& a, int b) {
+  Request r;
+  r.ell = a.vlen ? a.vlen[b] : a.L;
+  r.row0 = a.row_off ? a.row_off[b] : 0;
+  r.seat = a.h.counts ? (a.seats ? a.seats[b] : b) : -1;
+  r.m = a.mask ? (a.mask_rows ? a.mask_rows[b] : b) : -1;
+  r.sat = r.seat >= 0 && r.seat < a.h.seats;
+  r.rep = 1.f;
+  r.freq = r.pres = 0.f;
+  if (r.sat) {
+    if (a.h.repetition) r.rep = a.h.repetition[r.seat];
+    if (a.h.frequency) r.freq = a.h.frequency[r.seat];
+    if (a.h.presence) r.pres = a.h.presence[r.seat];
+  }
+  r.nrow = r.ell + a.rows - a.L;
+  r.flag = 0;
+  if (r.ell < 0 || r.ell > a.L) r.flag |= kFlagVerifyLen;
+  else if (a.row_off && (r.row0 < 0 || r.row0 + r.nrow > a.n_rows)) r.flag |= kFlagIndex;
+  if ((a.h.counts && r.seat >= a.h.seats) || (a.mask && r.m >= a.n_masks)) r.flag |= kFlagIndex;
+  if (!(r.rep > 0.f && r.rep < INFINITY && fabsf(r.freq) < INFINITY && fabsf(r.pres) < INFINITY)) r.flag |= kFlagParam;
+  r.pen = r.sat && (r.rep != 1.f || r.freq != 0.f || r.pres != 0.f);
+  return r;
+}
+// First byte of row q of the request, q = z * nrow + i (z: branch); i is the position.
+template <int DT>
+__device__ __forceinline__ int64_t row_byte(const RulesArgs& a, const Request& r, int b, int q, int& i) {
+  const int z = q / r.nrow;
+  i = q - z * r.nrow;
+  const int64_t row = a.row_off ? r.row0 + i : (static_cast<int64_t>(b) * a.K + z) * a.rows + i;
+  return row * a.V * Elem<DT>::kBytes;
+}
+
+// Block (x, b, z): 8192 tokens of kStreamRows rows, 1024 tokens to a warp.
+template <int DT, bool INPLACE>
+__global__ void __launch_bounds__(kThreads, SMINB) k_rules_stream(const RulesArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kChunk;
+  const Request r = load_request(a, b);
+  if (r.flag) {
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(a.status, r.flag);
+    return;
+  }
+  if (t0 >= a.V || (INPLACE && r.m < 0)) return;
+  const int span = static_cast<int>(min(static_cast<int64_t>(kChunk), a.V - t0));
+  const int64_t W = (a.V + 31) / 32, w = t0 / 32 + lane;
+  const int q0 = blockIdx.z * kStreamRows, nq = min(a.K * r.nrow - q0, kStreamRows);
+  const uint32_t* mask = a.mask + static_cast<int64_t>(r.m) * a.mask_len * W + w;
+  const bool masked = r.m >= 0 && w < W;
+  int next_i = 0;
+  int64_t next = nq > 0 ? row_byte<DT>(a, r, b, q0, next_i) : 0;
+  uint32_t next_allow = masked && nq > 0 ? mask[next_i * W] : 0xffffffffu;
+#pragma unroll 1
+  for (int k = 0; k < nq; ++k) {  // the next row's mask is on its way while this row is written
+    const int64_t off = next + t0 * Elem<DT>::kBytes;
+    const uint32_t allow = next_allow;
+    if (k + 1 < nq) {
+      next = row_byte<DT>(a, r, b, q0 + k + 1, next_i);
+      if (masked) next_allow = mask[next_i * W];
+    }
+    stream_chunk<DT, INPLACE>(a.x + off, a.out + off, span, allow);
+  }
+}
+
+// The drafted and biased tokens of a request ("special"), in dynamic shared
+// memory: entry e < 32 is drafted token e, entry 32 + k bias entry k.
+struct Special {
+  int* v;             // token, relative to the tile; negative: not in it
+  float* add;         // bias value; an owner's: the sum of its token's
+  uint32_t* drafted;  // an owner's: bit k, drafted at position k
+  int* count;         // an owner's: its count, -1 when not seen
+  int* twice;         // tokens that more than one entry names
+  uint16_t* owner;    // entries that speak for their token
+};
+constexpr int kSpecialBytes = 5 * 4 + 2;
+__device__ __forceinline__ Special carve_special(char* base, int n) {
+  Special s;
+  s.v = reinterpret_cast<int*>(base);
+  s.add = reinterpret_cast<float*>(s.v + n);
+  s.drafted = reinterpret_cast<uint32_t*>(s.add + n);
+  s.count = reinterpret_cast<int*>(s.drafted + n);
+  s.twice = s.count + n;
+  s.owner = reinterpret_cast<uint16_t*>(s.twice + n);
+  return s;
+}
+
+// Block (b, z): rows q0 .. q1 of request b over the whole vocabulary; reads
+// a.x, writes the named tokens of a.out.
 //
-// The ids of real histories crowd in the low end of the vocabulary. A block
-// therefore compacts its seen tokens into a list in shared memory and hands
-// them to its threads, spare threads taking further rows; a crowded tile is
-// spread over the whole block, and over further blocks by rows. Tokens that
-// are drafted or biased are taken out of the list and go a slower way.
-template <int DT, bool INPLACE, int WPT>
-__global__ void __launch_bounds__(kThreads, 6) k_logit_rules(const RulesArgs a) {
-  constexpr int kTile = WPT * 32 * kThreads;
+// The ids of real histories crowd in the low end of the vocabulary, so a
+// block takes all of it (in tiles of kEditTile tokens, one for most models):
+// it compacts the named tokens into a list in shared memory and spreads list x
+// rows over its threads, eight elements in flight per thread. Seen tokens
+// need their count alone; drafted and biased ones, whose value differs from
+// row to row or has a sum in it, come first in the list and go a slower way.
+template <int DT>
+__global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesArgs a) {
+  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 8;  // WPT words of the bit table per thread
   constexpr int es = Elem<DT>::kBytes;
-  __shared__ uint32_t s_word[WPT * kThreads];
-  __shared__ uint16_t s_list[kListMax];
-  __shared__ int64_t s_off[kRowsMax];  // first byte of a row
+  extern __shared__ __align__(16) char s_dyn[];
+  uint32_t* s_claim = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] bits of special tokens
+  int* s_list = reinterpret_cast<int*>(s_claim + WPT * NT);           // [kListMax]
+  float* s_minus = reinterpret_cast<float*>(s_list + kListMax);       // [kListMax] f c + p [c > 0] of the list's tokens
+  const Special sp = carve_special(reinterpret_cast<char*>(s_minus + kListMax), a.special);
+  __shared__ int64_t s_off[kRowsMax];     // first byte of a row
   __shared__ int16_t s_pos[kRowsMax];
-  __shared__ int s_tok[32 + SPEC_MAX_BIAS];  // drafted tokens, then the bias list
-  __shared__ float s_val[SPEC_MAX_BIAS];
-  __shared__ uint16_t s_special[32 + SPEC_MAX_BIAS];
-  __shared__ int s_n, s_ns;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.y;
+  __shared__ int s_n, s_nt, s_no;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int b = blockIdx.x;
   const int64_t V = a.V, W = (V + 31) / 32;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTile, w0 = t0 / 32;
-  const int span = static_cast<int>(min(static_cast<int64_t>(kTile), V - t0));
-  const bool first = blockIdx.z == 0 && blockIdx.x == 0;
-  if (tid == 0) s_n = s_ns = 0;
+  for (int w = tid; w < WPT * NT; w += NT) s_claim[w] = 0u;
+  if (tid == 0) s_n = s_nt = s_no = 0;
   pdl_wait();
   pdl_trigger();
 
-  // the request: a value outside its range leaves all its rows as they were
-  const int ell = a.vlen ? a.vlen[b] : a.L;
-  const int64_t row0 = a.row_off ? a.row_off[b] : 0;
-  const int seat = a.h.counts ? (a.seats ? a.seats[b] : b) : -1;
-  const int m = a.mask ? (a.mask_rows ? a.mask_rows[b] : b) : -1;
-  const bool sat = seat >= 0 && seat < a.h.seats;
-  float rep = 1.f, freq = 0.f, pres = 0.f;
-  uint32_t word[WPT];  // words tid, tid + 256, ... of the tile
-#pragma unroll
-  for (int k = 0; k < WPT; ++k) word[k] = 0u;
-  if (sat) {
-    if (a.h.repetition) rep = a.h.repetition[seat];
-    if (a.h.frequency) freq = a.h.frequency[seat];
-    if (a.h.presence) pres = a.h.presence[seat];
-    const uint32_t* seen = a.h.seen + seat * W + w0;
-#pragma unroll
-    for (int k = 0; k < WPT; ++k)
-      if ((tid + k * kThreads) * 32 < span) word[k] = seen[tid + k * kThreads];
-  }
-  const int nrow = ell + a.rows - a.L;
-  int flag = 0;
-  if (ell < 0 || ell > a.L) flag |= kFlagVerifyLen;
-  else if (a.row_off && (row0 < 0 || row0 + nrow > a.n_rows)) flag |= kFlagIndex;
-  if ((a.h.counts && seat >= a.h.seats) || (a.mask && m >= a.n_masks)) flag |= kFlagIndex;
-  if (!(rep > 0.f && rep < INFINITY && fabsf(freq) < INFINITY && fabsf(pres) < INFINITY)) flag |= kFlagParam;
-  if (flag) {
-    if (first && tid == 0) atomicOr(a.status, flag);
+  const Request r = load_request(a, b);
+  if (r.flag) {
+    if (blockIdx.y == 0 && tid == 0) atomicOr(a.status, r.flag);
     return;
   }
-  const bool pen = sat && (rep != 1.f || freq != 0.f || pres != 0.f);
-  const int n_bias = sat ? a.h.n_bias : 0, n_tok = pen ? ell : 0;
-  const int q0 = blockIdx.z * a.per, nq = min(a.K * nrow, q0 + a.per) - q0;
-  if (first && tid < n_tok) {
+  const bool pen = r.pen;
+  const int seat = r.seat, m = r.m;
+  const float rep = r.rep, freq = r.freq, pres = r.pres;
+  const int n_bias = r.sat ? a.h.n_bias : 0, n_tok = pen ? r.ell : 0;
+  const int q0 = blockIdx.y * a.per, nq = min(a.K * r.nrow, q0 + a.per) - q0;
+  if (blockIdx.y == 0 && tid < n_tok) {
     const int x = a.tokens[static_cast<int64_t>(b) * a.L + tid];
     if (x < 0 || x >= V) atomicOr(a.status, kFlagTokenRange);
   }
-  if (nq <= 0 || (INPLACE && !pen && m < 0 && n_bias == 0)) return;
-  for (int q = tid; q < nq; q += kThreads) {
-    const int z = (q0 + q) / nrow, i = q0 + q - z * nrow;
-    const int64_t r = a.row_off ? row0 + i : (static_cast<int64_t>(b) * a.K + z) * a.rows + i;
-    s_off[q] = r * V * es;
+  if (nq <= 0 || (!pen && n_bias == 0)) return;
+  const uint32_t* seen = a.h.seen + seat * W;
+  const int32_t* counts = a.h.counts + seat * V;
+  const uint32_t* mask = a.mask + (m >= 0 ? static_cast<int64_t>(m) * a.mask_len * W : 0);
+  for (int q = tid; q < nq; q += NT) {
+    int i;
+    s_off[q] = row_byte<DT>(a, r, b, q0 + q, i);
     s_pos[q] = static_cast<int16_t>(i);
   }
-  const uint32_t* mask = a.mask + (m >= 0 ? static_cast<int64_t>(m) * a.mask_len * W : 0);
-#pragma unroll
-  for (int k = 0; k < WPT; ++k) {
-    const int at = (tid + k * kThreads) * 32;
-    if (!pen) word[k] = 0u;
-    else if (at + 32 > span) word[k] &= at >= span ? 0u : (1u << (span - at)) - 1u;
-  }
 
-  // drafted and biased tokens of the tile: out of the list, into s_special
-  if (n_tok + n_bias > 0) {
-#pragma unroll
-    for (int k = 0; k < WPT; ++k) s_word[tid + k * kThreads] = word[k];
-  }
-  __syncthreads();  // s_n, s_ns, s_off, s_pos, s_word
-  if (n_tok + n_bias > 0) {
-    for (int e = tid; e < 32 + n_bias; e += kThreads) {
-      int x = -1;
-      if (e >= 32) {
-        x = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
-        s_val[e - 32] = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
-        if (first && x >= V) atomicOr(a.status, kFlagTokenRange);
-      } else if (e < n_tok) {
-        x = a.tokens[static_cast<int64_t>(b) * a.L + e];
-      }
-      s_tok[e] = x;
-      if (x >= t0 && x < t0 + span) {
-        s_special[atomicAdd(&s_ns, 1)] = static_cast<uint16_t>(e);
-        atomicAnd(&s_word[(x - t0) >> 5], ~(1u << (x & 31)));
-      }
+  for (int64_t t0 = 0; t0 < V; t0 += kEditTile) {
+    const int span = static_cast<int>(min(static_cast<int64_t>(kEditTile), V - t0));
+    const int64_t w0 = t0 / 32;
+    if (t0) {  // a further tile: the last one's shared memory is free
+      __syncthreads();
+      for (int w = tid; w < WPT * NT; w += NT) s_claim[w] = 0u;
+      if (tid == 0) s_n = s_nt = s_no = 0;
     }
-    __syncthreads();
+    uint32_t word[WPT];  // words tid, tid + NT, ... of the tile
 #pragma unroll
-    for (int k = 0; k < WPT; ++k) word[k] = s_word[tid + k * kThreads];
-  }
-  int mine = 0;
-#pragma unroll
-  for (int k = 0; k < WPT; ++k) mine += __popc(word[k]);
-  int rank = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, rank, o);
-    if (lane >= o) rank += t;
-  }
-  int base = 0;
-  if (lane == 31 && rank) base = atomicAdd(&s_n, rank);  // the warps' order is free: tokens are independent
-  rank = __shfl_sync(0xffffffffu, base, 31) + rank - mine;
-
-  if (!INPLACE || m >= 0) {
-    for (int c = warp; c * kChunk < span; c += kWarps) {
-      const int wspan = min(kChunk, span - c * kChunk);
-      const int64_t w = w0 + c * 32 + lane;
-      for (int q = 0; q < nq; ++q) {
-        const uint32_t allow = m >= 0 && w < W ? mask[s_pos[q] * W + w] : 0xffffffffu;
-        const int64_t off = s_off[q] + (t0 + c * kChunk) * es;
-        stream_chunk<DT, INPLACE>(a.x + off, a.out + off, wspan, allow);
-      }
+    for (int k = 0; k < WPT; ++k) {
+      const int at = (tid + k * NT) * 32;
+      word[k] = pen && at < span ? seen[w0 + tid + k * NT] : 0u;
     }
-  }
-
-  // the list, in rounds of kListMax tokens (one, unless the history holds most of the vocabulary)
-  __syncthreads();  // s_n; out of place: the copies come before the edits
-  const int n = s_n;
-  for (int l0 = 0; l0 < n; l0 += kListMax) {
-    if (l0) __syncthreads();
-    int at = rank - l0;
-#pragma unroll
-    for (int k = 0; k < WPT; ++k)
-      for (uint32_t left = word[k]; left; left &= left - 1, ++at)
-        if (at >= 0 && at < kListMax)
-          s_list[at] = static_cast<uint16_t>((tid + k * kThreads) * 32 + __ffs(left) - 1);
-    __syncthreads();
-    const int ln = min(kListMax, n - l0);
-    for (int e0 = 0; e0 < ln; e0 += kThreads) {
-      const int take = min(kThreads, ln - e0);
-      const int groups = kThreads / take, sub = tid / take;
-      if (sub >= groups) continue;
-      const int64_t v = t0 + s_list[e0 + tid - sub * take];
-      const int c = a.h.counts[seat * V + v];
-      const char* x = a.x + v * es;
-      char* y = a.out + v * es;
-      for (int q = sub; q < nq; q += 4 * groups) {  // four rows' loads in flight
-        float f[4];
-        bool on[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = q + k * groups;
-          on[k] = r < nq;
-          if (on[k] && m >= 0) on[k] = mask[s_pos[r] * W + (v >> 5)] >> (v & 31) & 1;
-          if (on[k]) f[k] = load_x<DT>(x + s_off[r], 0);
+    __syncthreads();  // s_claim, s_n, s_nt, s_no, s_off, s_pos
+    if (n_tok + n_bias > 0) {
+      uint32_t mine = 0u;  // entries this thread was the first to name
+      for (int e = tid, j = 0; e < 32 + n_bias; e += NT, ++j) {
+        int64_t x = -1;
+        float add = 0.f;
+        if (e >= 32) {
+          x = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
+          add = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
+          if (blockIdx.y == 0 && t0 == 0 && x >= V) atomicOr(a.status, kFlagTokenRange);
+        } else if (e < n_tok) {
+          x = a.tokens[static_cast<int64_t>(b) * a.L + e];
         }
-        const float minus = freq * static_cast<float>(c) + (c > 0 ? pres : 0.f);
+        const bool in = x >= t0 && x < t0 + span;
+        const int v = in ? static_cast<int>(x - t0) : -1;
+        sp.v[e] = v;
+        sp.add[e] = add;
+        if (in) {
+          const uint32_t bit = 1u << (v & 31);
+          if (atomicOr(&s_claim[v >> 5], bit) & bit) sp.twice[atomicAdd(&s_nt, 1)] = v;
+          else mine |= 1u << j;
+        }
+      }
+      __syncthreads();
+      // One entry of a token, whichever came first, speaks for it: it collects the positions the token is drafted at
+      // and its biases, added up in list order.
+      const int nt = s_nt;
+      for (int e = tid, j = 0; e < 32 + n_bias; e += NT, ++j) {
+        if (!(mine >> j & 1)) continue;
+        const int v = sp.v[e];
+        uint32_t drafted = e < 32 ? 1u << e : 0u;
+        const bool was = pen && (seen[w0 + (v >> 5)] >> (v & 31) & 1);
+        const int count = was ? counts[t0 + v] : -1;
+        bool more = false;
+        for (int k = 0; k < nt; ++k) more |= sp.twice[k] == v;
+        if (more) {
+          float add = 0.f;
+          for (int k = 0; k < n_tok; ++k) drafted |= (sp.v[k] == v ? 1u : 0u) << k;
+          for (int k = 32; k < 32 + n_bias; ++k)
+            if (sp.v[k] == v) add += sp.add[k];
+          sp.add[e] = add;  // no other thread reads the entries of this token
+        }
+        sp.drafted[e] = drafted;
+        sp.count[e] = count;
+        sp.owner[atomicAdd(&s_no, 1)] = static_cast<uint16_t>(e);
+      }
+    }
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) {
+      const int left = span - (tid + k * NT) * 32;
+      word[k] &= ~s_claim[tid + k * NT];
+      if (left < 32) word[k] &= left <= 0 ? 0u : (1u << left) - 1u;
+      mine += __popc(word[k]);
+    }
+    int rank = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, rank, o);
+      if (lane >= o) rank += t;
+    }
+    int base = 0;
+    if (lane == 31 && rank) base = atomicAdd(&s_n, rank);  // the warps' order is free: tokens are independent
+    rank = __shfl_sync(0xffffffffu, base, 31) + rank - mine;
+
+    // named tokens x rows; the list in rounds of kListMax (one, unless the history is very long)
+    __syncthreads();  // s_n, s_no
+    const int n = s_n, no = s_no;
+    for (int l0 = 0; l0 == 0 || l0 < n; l0 += kListMax) {
+      const int ln = min(kListMax, n - l0), first_e = l0 == 0 ? no : 0, ne = ln + first_e;
+      if (ne == 0) break;
+      if (l0) __syncthreads();
+      int at = rank - l0;
+#pragma unroll
+      for (int k = 0; k < WPT; ++k)
+        for (uint32_t left = word[k]; left; left &= left - 1, ++at)
+          if (at >= 0 && at < kListMax) s_list[at] = (tid + k * NT) * 32 + __ffs(left) - 1;
+      __syncthreads();
+      for (int e = tid; e < ln; e += 4 * NT) {
+        int c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = e + k * NT < ln ? counts[t0 + s_list[e + k * NT]] : 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (on[k]) store_x<DT>(y + s_off[q + k * groups], 0, (f[k] > 0.f ? f[k] / rep : f[k] * rep) - minus);
+          if (e + k * NT < ln) s_minus[e + k * NT] = freq * static_cast<float>(c[k]) + (c[k] > 0 ? pres : 0.f);
       }
-    }
-  }
-
-  // drafted and biased tokens: the first of the entries that name a token speaks for all, in list order
-  const int ns = s_ns;
-  for (int e0 = 0; e0 < ns; e0 += kThreads) {
-    const int take = min(kThreads, ns - e0);
-    const int groups = kThreads / take, sub = tid / take;
-    if (sub >= groups) continue;
-    const int self = s_special[e0 + tid - sub * take];
-    const int64_t v = s_tok[self];
-    uint32_t drafted = 0u;
-    bool mute = false;
-    for (int k = 0; k < n_tok; ++k)
-      if (s_tok[k] == v) {
-        drafted |= 1u << k;
-        mute |= k < self;
+      if (ln > 0) __syncthreads();
+      const int dq = NT / ne, de = NT - dq * ne;  // a step of NT elements
+      int e = tid % ne, q = tid / ne;
+      const char* x = a.x + t0 * es;
+      char* y = a.out + t0 * es;
+      while (q < nq) {
+        float f[kBatch];
+        uint32_t on = 0u;
+        int e2 = e, q2 = q;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (q < nq) {
+            const int v = e < first_e ? sp.v[sp.owner[e]] : s_list[e - first_e];
+            if (m < 0 || (mask[s_pos[q] * W + w0 + (v >> 5)] >> (v & 31) & 1)) {
+              on |= 1u << k;
+              f[k] = load_x<DT>(x + s_off[q], v);
+            }
+          }
+          q += dq;
+          e += de;
+          if (e >= ne) {
+            e -= ne;
+            ++q;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (on >> k & 1) {
+            if (e2 >= first_e) {
+              const int v = s_list[e2 - first_e];
+              store_x<DT>(y + s_off[q2], v, (f[k] > 0.f ? f[k] / rep : f[k] * rep) - s_minus[e2 - first_e]);
+            } else {
+              const int o = sp.owner[e2], i = s_pos[q2];
+              const int extra = __popc(sp.drafted[o] & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
+              const int c = max(sp.count[o], 0) + extra;
+              const bool known = sp.count[o] >= 0 || extra > 0;
+              const float add = sp.add[o];
+              if (known || add != 0.f) {
+                const float g = known ? (f[k] > 0.f ? f[k] / rep : f[k] * rep) : f[k];
+                store_x<DT>(y + s_off[q2], sp.v[o], g - (freq * static_cast<float>(c) + (c > 0 ? pres : 0.f)) + add);
+              }
+            }
+          }
+          q2 += dq;
+          e2 += de;
+          if (e2 >= ne) {
+            e2 -= ne;
+            ++q2;
+          }
+        }
       }
-    float add = 0.f;
-    for (int k = 0; k < n_bias && !mute; ++k)
-      if (s_tok[32 + k] == v) {
-        add += s_val[k];
-        mute = 32 + k < self;
-      }
-    if (mute) continue;
-    const bool seen = pen && (a.h.seen[seat * W + (v >> 5)] >> (v & 31) & 1);
-    const int count = seen ? a.h.counts[seat * V + v] : 0;
-    for (int q = sub; q < nq; q += groups) {
-      const int i = s_pos[q];
-      const int extra = __popc(drafted & (i >= 32 ? 0xffffffffu : (1u << i) - 1u)), c = count + extra;
-      const bool known = seen || extra > 0;
-      if (!known && add == 0.f) continue;
-      if (m >= 0 && !(mask[i * W + (v >> 5)] >> (v & 31) & 1)) continue;
-      const float f = load_x<DT>(a.x + s_off[q], v);
-      const float g = known ? (f > 0.f ? f / rep : f * rep) : f;
-      store_x<DT>(a.out + s_off[q], v, g - freq * static_cast<float>(c) - (c > 0 ? pres : 0.f) + add);
     }
   }
 }
 
-template <int WPT>
-cudaError_t launch_tiles(RulesArgs a, int dtype, cudaStream_t st) {
-  const int64_t x = (a.V + WPT * 32 * kThreads - 1) / (WPT * 32 * kThreads);
+cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st) {
+  RulesArgs a = args;
   const int most = a.K * a.rows;
-  const int64_t want = 148 * 12;  // two waves of 6 blocks on 148 SMs, by splitting rows
-  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, want / (x * a.B))));
-  a.per = (most + z - 1) / z;
-  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));
   const bool inplace = a.x == a.out;
-  void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_logit_rules<0, true, WPT> : k_logit_rules<0, false, WPT>)
-                                    : (inplace ? k_logit_rules<1, true, WPT> : k_logit_rules<1, false, WPT>);
-  return launch_pdl(k, grid, dim3(kThreads), 0, st, a);
-}
-
-cudaError_t launch_logit_rules(const RulesArgs& a, int dtype, cudaStream_t st) {
-  const bool streams = a.x != a.out || a.mask;
-  return streams ? launch_tiles<1>(a, dtype, st) : launch_tiles<4>(a, dtype, st);
+  if (!inplace || a.mask) {
+    const dim3 grid(static_cast<unsigned>((a.V + kWarps * kChunk - 1) / (kWarps * kChunk)), static_cast<unsigned>(a.B),
+                    static_cast<unsigned>((most + kStreamRows - 1) / kStreamRows));
+    void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_rules_stream<0, true> : k_rules_stream<0, false>)
+                                      : (inplace ? k_rules_stream<1, true> : k_rules_stream<1, false>);
+    const cudaError_t e = launch_pdl(k, grid, dim3(kThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.h.counts) return cudaSuccess;
+  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * WANT / a.B)));
+  a.per = (most + z - 1) / z;
+  a.special = 32 + a.h.n_bias;
+  const dim3 grid(static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));
+  const size_t smem = kEditTile / 8 + kListMax * 8 + static_cast<size_t>(a.special) * kSpecialBytes;
+  void (*k)(RulesArgs) = dtype == 0 ? k_rules_edit<0> : k_rules_edit<1>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_pdl(k, grid, dim3(kEditThreads), smem, st, a);
 }
 
 // ------------------------------------------------------------------ history

@@ -29,7 +29,8 @@ struct RulesArgs {
   const uint32_t* mask;     // nullable
   const int32_t* mask_rows; // nullable
   int n_masks, mask_len;
-  int per;                  // rows of a request that one warp takes
+  int per;                  // rows of a request that one block takes
+  int special;              // room for drafted and biased tokens
   int* status;
 };
 
