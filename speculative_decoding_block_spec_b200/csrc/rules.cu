@@ -23,17 +23,16 @@ namespace specv {
 #ifndef MINB
 #define MINB 2
 #endif
-#ifndef SMINB
-#define SMINB 6
+#ifndef SPI
+#define SPI 4
 #endif
-#ifndef SROWS
-#define SROWS 4
+#ifndef SPO
+#define SPO 1
 #endif
 #ifndef WANT
 #define WANT 4
 #endif
 constexpr int kChunk = 1024;  // tokens of one warp's step over a row: 32 words of a bit table
-constexpr int kStreamRows = SROWS;
 constexpr int kEditThreads = 512;
 constexpr int kEditTile = 10 * 32 * kEditThreads;  // tokens of the edit kernel's tile: 163,840
 constexpr int kListMax = 4096;  // seen tokens that are taken at a time
@@ -67,8 +66,8 @@ template <int DT> __device__ __forceinline__ uint4 neg_inf16() {
   return make_uint4(w, w, w, w);
 }
 
-// Words of `allow` whose groups of E bits are all 0 keep those bits: the
-// 16-byte vectors that are forbidden as a whole.
+// The lowest bit of every group of E bits of `forbid` that is all ones: the
+// 16-byte vectors that are forbidden whole.
 template <int E> __device__ __forceinline__ uint32_t whole_groups(uint32_t forbid) {
   uint32_t t = forbid & (forbid >> 1);
   t &= t >> 2;
@@ -90,13 +89,34 @@ template <int DT> __device__ __forceinline__ uint4 choose(const uint4& v, uint32
   }
 }
 
+// In place, vectors that the mask forbids in part, read, changed and written
+// back (their other elements are this warp's alone). Kept out of line: few
+// masks need it, and it would cost the others registers.
+template <int DT>
+__device__ __noinline__ void mask_partial(char* dst, int nvec, uint32_t ok) {
+  constexpr int E = Elem<DT>::kPerVec;
+  const int lane = threadIdx.x & 31;
+  for (int t = 0; t < kChunk / E / 32; ++t) {
+    const uint32_t g = __shfl_sync(0xffffffffu, ok, lane / (32 / E) + t * E) >> (lane % (32 / E) * E) & ((1u << E) - 1u);
+    uint4* at = reinterpret_cast<uint4*>(dst + t * 32 * 16);
+    if (lane + 32 * t < nvec && g != 0u && g != (1u << E) - 1u) *at = choose<DT>(*at, g);
+  }
+}
+
 // One warp's 1024 tokens of one row: -inf where the mask forbids and, out of
 // place, the copy. `allow`: the lane's 32 tokens of the mask. 16-byte vectors
-// at the output's alignment (the mask is shifted to it), elements at the ends;
-// in place, vectors that are forbidden only in part are written by elements.
+// at the output's alignment (the mask is shifted to it), elements at the ends.
+//
+// In place, vectors that are forbidden whole are stored whole, and those that
+// are forbidden in part by elements while a lane has at most kPops stores to
+// make, else by reading them. 544 rows of 151,936 bf16 tokens, us:
+//   forbidden            by elements   by reading
+//   2 % at random             34           59
+//   all but 100 tokens        37           41
+//   half, at random          217           72
 template <int DT, bool INPLACE>
 __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int span, uint32_t allow) {
-  constexpr int es = Elem<DT>::kBytes, E = Elem<DT>::kPerVec, NV = kChunk / E / 32;
+  constexpr int es = Elem<DT>::kBytes, E = Elem<DT>::kPerVec, NV = kChunk / E / 32, kPops = 8;
   const int lane = threadIdx.x & 31;
   const bool vec = INPLACE || ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
   if (!vec) {
@@ -113,7 +133,7 @@ __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int spa
   const int nvec = (span - head) / E;
   src += (head + lane * E) * es;  // the lane's first vector
   dst += (head + lane * E) * es;
-  constexpr int kStep = 32 * 16, kFly = 4;  // vectors in flight per lane
+  constexpr int kStep = 32 * 16, kFly = 4;  // bytes from vector to vector; vectors in flight per lane
   uint4 v[kFly];
   if constexpr (!INPLACE) {
 #pragma unroll
@@ -121,7 +141,6 @@ __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int spa
       if (lane + 32 * t < nvec) v[t] = ldg16(src + t * kStep);
   }
   uint32_t ok = allow;  // bit i: token head + 32 lane + i
-  const uint32_t ends = __shfl_sync(0xffffffffu, allow, 0);
   if (head) {
     const uint32_t next = __shfl_down_sync(0xffffffffu, allow, 1);
     ok = __funnelshift_r(ok, lane == 31 ? 0xffffffffu : next, head);
@@ -137,10 +156,23 @@ __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int spa
         if (__shfl_sync(0xffffffffu, whole, from + t * E) >> at & 1)
           *reinterpret_cast<uint4*>(dst + t * kStep) = neg_inf16<DT>();
     }
-    dst += 32 * lane * es - lane * 16;  // the lane's 32 tokens
-    for (uint32_t part = ~ok & ~(whole * ((1u << E) - 1u)); part; part &= part - 1)
-      store_x<DT>(dst, __ffs(part) - 1, -INFINITY);
-    if (lane < head && !(ends >> lane & 1)) store_x<DT>(dst, lane - head - 32 * lane, -INFINITY);
+    uint32_t part = ~ok & ~(whole * ((1u << E) - 1u));
+    uint32_t two = DT == 1 ? part & part >> 1 & 0x55555555u : 0u;  // aligned bf16 pairs
+    if (__any_sync(0xffffffffu, __popc(part) - __popc(two) > kPops)) {
+      mask_partial<DT>(dst, nvec, ok);
+      // what is left are the elements behind the last vector
+      const int behind = nvec * E - 32 * lane;
+      part &= behind >= 32 ? 0u : behind <= 0 ? 0xffffffffu : 0xffffffffu << behind;
+      two &= part;  // a pair lies on one side: nvec * E is even
+    }
+    char* own = dst + 32 * lane * es - lane * 16;  // the lane's 32 tokens
+    part &= ~(two * 3u);
+    for (; two; two &= two - 1) *reinterpret_cast<uint32_t*>(own + (__ffs(two) - 1) * es) = 0xff80ff80u;
+    for (; part; part &= part - 1) store_x<DT>(own, __ffs(part) - 1, -INFINITY);
+    if (head) {
+      const uint32_t ends = __shfl_sync(0xffffffffu, allow, 0);
+      if (lane < head && !(ends >> lane & 1)) store_x<DT>(dst, lane - head - lane * E, -INFINITY);
+    }
   } else {
     const bool plain = __all_sync(0xffffffffu, ok == 0xffffffffu);
 #pragma unroll
@@ -204,9 +236,9 @@ __device__ __forceinline__ int64_t row_byte(const RulesArgs& a, const Request& r
   return row * a.V * Elem<DT>::kBytes;
 }
 
-// Block (x, b, z): 8192 tokens of kStreamRows rows, 1024 tokens to a warp.
+// Block (x, b, z): 8192 tokens, 1024 to a warp, of `per` rows of request b.
 template <int DT, bool INPLACE>
-__global__ void __launch_bounds__(kThreads, SMINB) k_rules_stream(const RulesArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) k_rules_stream(const RulesArgs a) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
@@ -216,24 +248,26 @@ __global__ void __launch_bounds__(kThreads, SMINB) k_rules_stream(const RulesArg
     if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(a.status, r.flag);
     return;
   }
-  if (t0 >= a.V || (INPLACE && r.m < 0)) return;
+  const int q0 = blockIdx.z * a.per, nq = min(a.K * r.nrow - q0, a.per);
+  if (t0 >= a.V || nq <= 0 || (INPLACE && r.m < 0)) return;
   const int span = static_cast<int>(min(static_cast<int64_t>(kChunk), a.V - t0));
-  const int64_t W = (a.V + 31) / 32, w = t0 / 32 + lane;
-  const int q0 = blockIdx.z * kStreamRows, nq = min(a.K * r.nrow - q0, kStreamRows);
-  const uint32_t* mask = a.mask + static_cast<int64_t>(r.m) * a.mask_len * W + w;
+  const int64_t W = (a.V + 31) / 32, w = t0 / 32 + lane, pitch = a.V * Elem<DT>::kBytes;
   const bool masked = r.m >= 0 && w < W;
-  int next_i = 0;
-  int64_t next = nq > 0 ? row_byte<DT>(a, r, b, q0, next_i) : 0;
-  uint32_t next_allow = masked && nq > 0 ? mask[next_i * W] : 0xffffffffu;
+  int i;
+  int64_t off = row_byte<DT>(a, r, b, q0, i) + t0 * Elem<DT>::kBytes;
+  const uint32_t* mask = a.mask + static_cast<int64_t>(r.m) * a.mask_len * W + w;
+  uint32_t next = masked ? mask[i * W] : 0xffffffffu;
 #pragma unroll 1
   for (int k = 0; k < nq; ++k) {  // the next row's mask is on its way while this row is written
-    const int64_t off = next + t0 * Elem<DT>::kBytes;
-    const uint32_t allow = next_allow;
-    if (k + 1 < nq) {
-      next = row_byte<DT>(a, r, b, q0 + k + 1, next_i);
-      if (masked) next_allow = mask[next_i * W];
+    const uint32_t allow = next;
+    const int64_t at = off;
+    off += pitch;
+    if (++i == r.nrow) {  // the next branch
+      i = 0;
+      off += (a.rows - r.nrow) * pitch;
     }
-    stream_chunk<DT, INPLACE>(a.x + off, a.out + off, span, allow);
+    if (masked && k + 1 < nq) next = mask[i * W];
+    stream_chunk<DT, INPLACE>(a.x + at, a.out + at, span, allow);
   }
 }
 
@@ -273,7 +307,8 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
   constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 8;  // WPT words of the bit table per thread
   constexpr int es = Elem<DT>::kBytes;
   extern __shared__ __align__(16) char s_dyn[];
-  uint32_t* s_claim = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] bits of special tokens
+  uint32_t* s_word = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] the tile's seen bits
+  uint32_t* s_claim = s_word + WPT * NT;                              // [WPT * NT] bits of special tokens
   int* s_list = reinterpret_cast<int*>(s_claim + WPT * NT);           // [kListMax]
   float* s_minus = reinterpret_cast<float*>(s_list + kListMax);       // [kListMax] f c + p [c > 0] of the list's tokens
   const Special sp = carve_special(reinterpret_cast<char*>(s_minus + kListMax), a.special);
@@ -283,7 +318,8 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
   const int tid = threadIdx.x, lane = tid & 31;
   const int b = blockIdx.x;
   const int64_t V = a.V, W = (V + 31) / 32;
-  for (int w = tid; w < WPT * NT; w += NT) s_claim[w] = 0u;
+  const bool special = a.L + a.h.n_bias > 0;
+  for (int w = tid; special && w < WPT * NT; w += NT) s_claim[w] = 0u;
   if (tid == 0) s_n = s_nt = s_no = 0;
   pdl_wait();
   pdl_trigger();
@@ -295,7 +331,8 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
   }
   const bool pen = r.pen;
   const int seat = r.seat, m = r.m;
-  const float rep = r.rep, freq = r.freq, pres = r.pres;
+  // x / r as x times the rounded 1 / r: one more rounding of 2^-24, for a division less per element
+  const float rep = r.rep, inv = 1.f / r.rep, freq = r.freq, pres = r.pres;
   const int n_bias = r.sat ? a.h.n_bias : 0, n_tok = pen ? r.ell : 0;
   const int q0 = blockIdx.y * a.per, nq = min(a.K * r.nrow, q0 + a.per) - q0;
   if (blockIdx.y == 0 && tid < n_tok) {
@@ -317,28 +354,37 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
     const int64_t w0 = t0 / 32;
     if (t0) {  // a further tile: the last one's shared memory is free
       __syncthreads();
-      for (int w = tid; w < WPT * NT; w += NT) s_claim[w] = 0u;
+      for (int w = tid; special && w < WPT * NT; w += NT) s_claim[w] = 0u;
       if (tid == 0) s_n = s_nt = s_no = 0;
     }
-    uint32_t word[WPT];  // words tid, tid + NT, ... of the tile
+    {
+      uint32_t word[WPT];
 #pragma unroll
-    for (int k = 0; k < WPT; ++k) {
-      const int at = (tid + k * NT) * 32;
-      word[k] = pen && at < span ? seen[w0 + tid + k * NT] : 0u;
+      for (int k = 0; k < WPT; ++k) word[k] = pen && (tid + k * NT) * 32 < span ? seen[w0 + tid + k * NT] : 0u;
+#pragma unroll
+      for (int k = 0; k < WPT; ++k) s_word[tid + k * NT] = word[k];
     }
+    int64_t entry = -1;  // special entry tid, loaded together with the words
+    float value = 0.f;
+    auto load_entry = [&](int e) {
+      entry = -1;
+      value = 0.f;
+      if (e < 32) {
+        if (e < n_tok) entry = a.tokens[static_cast<int64_t>(b) * a.L + e];
+      } else if (e < 32 + n_bias) {
+        entry = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
+        value = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
+      }
+    };
+    load_entry(tid);
     __syncthreads();  // s_claim, s_n, s_nt, s_no, s_off, s_pos
     if (n_tok + n_bias > 0) {
       uint32_t mine = 0u;  // entries this thread was the first to name
       for (int e = tid, j = 0; e < 32 + n_bias; e += NT, ++j) {
-        int64_t x = -1;
-        float add = 0.f;
-        if (e >= 32) {
-          x = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
-          add = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
-          if (blockIdx.y == 0 && t0 == 0 && x >= V) atomicOr(a.status, kFlagTokenRange);
-        } else if (e < n_tok) {
-          x = a.tokens[static_cast<int64_t>(b) * a.L + e];
-        }
+        if (j) load_entry(e);
+        const int64_t x = entry;
+        const float add = value;
+        if (e >= 32 && x >= V && blockIdx.y == 0 && t0 == 0) atomicOr(a.status, kFlagTokenRange);
         const bool in = x >= t0 && x < t0 + span;
         const int v = in ? static_cast<int>(x - t0) : -1;
         sp.v[e] = v;
@@ -357,8 +403,9 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
         if (!(mine >> j & 1)) continue;
         const int v = sp.v[e];
         uint32_t drafted = e < 32 ? 1u << e : 0u;
-        const bool was = pen && (seen[w0 + (v >> 5)] >> (v & 31) & 1);
-        const int count = was ? counts[t0 + v] : -1;
+        const uint32_t bits = pen ? seen[w0 + (v >> 5)] : 0u;
+        const int stored = pen ? counts[t0 + v] : 0;  // on its way beside the bits: 0 where the bit is not set
+        const int count = bits >> (v & 31) & 1 ? stored : -1;
         bool more = false;
         for (int k = 0; k < nt; ++k) more |= sp.twice[k] == v;
         if (more) {
@@ -374,12 +421,15 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
       }
     }
     int mine = 0;
-#pragma unroll
-    for (int k = 0; k < WPT; ++k) {
-      const int left = span - (tid + k * NT) * 32;
-      word[k] &= ~s_claim[tid + k * NT];
-      if (left < 32) word[k] &= left <= 0 ? 0u : (1u << left) - 1u;
-      mine += __popc(word[k]);
+#pragma unroll 1
+    for (int w = tid; w < WPT * NT; w += NT) {
+      const int left = span - w * 32;
+      if (left <= 0) break;
+      uint32_t bits = s_word[w];
+      if (special) bits &= ~s_claim[w];
+      if (left < 32) bits &= (1u << left) - 1u;
+      s_word[w] = bits;
+      mine += __popc(bits);
     }
     int rank = mine;
 #pragma unroll
@@ -395,36 +445,29 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
     __syncthreads();  // s_n, s_no
     const int n = s_n, no = s_no;
     for (int l0 = 0; l0 == 0 || l0 < n; l0 += kListMax) {
-      const int ln = min(kListMax, n - l0), first_e = l0 == 0 ? no : 0, ne = ln + first_e;
-      if (ne == 0) break;
+      const int ln = min(kListMax, n - l0);
+      if (ln == 0 && no == 0) break;
       if (l0) __syncthreads();
-      int at = rank - l0;
-#pragma unroll
-      for (int k = 0; k < WPT; ++k)
-        for (uint32_t left = word[k]; left; left &= left - 1, ++at)
-          if (at >= 0 && at < kListMax) s_list[at] = (tid + k * NT) * 32 + __ffs(left) - 1;
-      __syncthreads();
-      for (int e = tid; e < ln; e += 4 * NT) {
-        int c[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = e + k * NT < ln ? counts[t0 + s_list[e + k * NT]] : 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (e + k * NT < ln) s_minus[e + k * NT] = freq * static_cast<float>(c[k]) + (c[k] > 0 ? pres : 0.f);
+      if (ln > 0) {
+        int at = rank - l0;
+#pragma unroll 1
+        for (int w = tid; w * 32 < span; w += NT)
+          for (uint32_t left = s_word[w]; left; left &= left - 1, ++at)
+            if (at >= 0 && at < kListMax) s_list[at] = w * 32 + __ffs(left) - 1;
+        __syncthreads();
       }
-      if (ln > 0) __syncthreads();
-      const int dq = NT / ne, de = NT - dq * ne;  // a step of NT elements
-      int e = tid % ne, q = tid / ne;
       const char* x = a.x + t0 * es;
       char* y = a.out + t0 * es;
-      while (q < nq) {
+      const int dq = ln ? NT / ln : 0, de = NT - dq * ln;  // a step of NT elements
+      int e = ln ? tid % ln : 0, q = ln ? tid / ln : nq;
+      for (bool begin = true;; begin = false) {
         float f[kBatch];
         uint32_t on = 0u;
         int e2 = e, q2 = q;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           if (q < nq) {
-            const int v = e < first_e ? sp.v[sp.owner[e]] : s_list[e - first_e];
+            const int v = s_list[e];
             if (m < 0 || (mask[s_pos[q] * W + w0 + (v >> 5)] >> (v & 31) & 1)) {
               on |= 1u << k;
               f[k] = load_x<DT>(x + s_off[q], v);
@@ -432,36 +475,47 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
           }
           q += dq;
           e += de;
-          if (e >= ne) {
-            e -= ne;
+          if (e >= ln) {
+            e -= ln;
             ++q;
           }
         }
+        if (begin) {  // while the first elements are on their way: special tokens, then the counts
+#pragma unroll 1
+          for (int j = tid; j < no * nq; j += NT) {
+            const int row = j / no, o = sp.owner[j - row * no], v = sp.v[o], i = s_pos[row];
+            const int extra = __popc(sp.drafted[o] & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
+            const int c = max(sp.count[o], 0) + extra;
+            const bool known = sp.count[o] >= 0 || extra > 0;
+            const float add = sp.add[o];
+            if ((!known && add == 0.f) || l0) continue;
+            if (m >= 0 && !(mask[i * W + w0 + (v >> 5)] >> (v & 31) & 1)) continue;
+            const float g = load_x<DT>(x + s_off[row], v);
+            store_x<DT>(y + s_off[row], v, (known ? g * (g > 0.f ? inv : rep) : g) -
+                                               (freq * static_cast<float>(c) + (c > 0 ? pres : 0.f)) + add);
+          }
+#pragma unroll 1
+          for (int j = tid; j < ln; j += 4 * NT) {
+            int c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = j + k * NT < ln ? counts[t0 + s_list[j + k * NT]] : 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (j + k * NT < ln) s_minus[j + k * NT] = freq * static_cast<float>(c[k]) + (c[k] > 0 ? pres : 0.f);
+          }
+          __syncthreads();
+        }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          if (on >> k & 1) {
-            if (e2 >= first_e) {
-              const int v = s_list[e2 - first_e];
-              store_x<DT>(y + s_off[q2], v, (f[k] > 0.f ? f[k] / rep : f[k] * rep) - s_minus[e2 - first_e]);
-            } else {
-              const int o = sp.owner[e2], i = s_pos[q2];
-              const int extra = __popc(sp.drafted[o] & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
-              const int c = max(sp.count[o], 0) + extra;
-              const bool known = sp.count[o] >= 0 || extra > 0;
-              const float add = sp.add[o];
-              if (known || add != 0.f) {
-                const float g = known ? (f[k] > 0.f ? f[k] / rep : f[k] * rep) : f[k];
-                store_x<DT>(y + s_off[q2], sp.v[o], g - (freq * static_cast<float>(c) + (c > 0 ? pres : 0.f)) + add);
-              }
-            }
-          }
+          if (on >> k & 1) store_x<DT>(y + s_off[q2], s_list[e2], f[k] * (f[k] > 0.f ? inv : rep) - s_minus[e2]);
           q2 += dq;
           e2 += de;
-          if (e2 >= ne) {
-            e2 -= ne;
+          if (e2 >= ln) {
+            e2 -= ln;
             ++q2;
           }
         }
+        if (q >= nq) break;
       }
     }
   }
@@ -472,8 +526,10 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   const int most = a.K * a.rows;
   const bool inplace = a.x == a.out;
   if (!inplace || a.mask) {
-    const dim3 grid(static_cast<unsigned>((a.V + kWarps * kChunk - 1) / (kWarps * kChunk)), static_cast<unsigned>(a.B),
-                    static_cast<unsigned>((most + kStreamRows - 1) / kStreamRows));
+    const int64_t x = (a.V + kWarps * kChunk - 1) / (kWarps * kChunk);
+    a.per = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(inplace ? SPI : SPO, x * a.B * most / (148 * 6))));
+    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.B),
+                    static_cast<unsigned>((most + a.per - 1) / a.per));
     void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_rules_stream<0, true> : k_rules_stream<0, false>)
                                       : (inplace ? k_rules_stream<1, true> : k_rules_stream<1, false>);
     const cudaError_t e = launch_pdl(k, grid, dim3(kThreads), 0, st, a);
@@ -484,7 +540,7 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   a.per = (most + z - 1) / z;
   a.special = 32 + a.h.n_bias;
   const dim3 grid(static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));
-  const size_t smem = kEditTile / 8 + kListMax * 8 + static_cast<size_t>(a.special) * kSpecialBytes;
+  const size_t smem = kEditTile / 4 + kListMax * 8 + static_cast<size_t>(a.special) * kSpecialBytes;
   void (*k)(RulesArgs) = dtype == 0 ? k_rules_edit<0> : k_rules_edit<1>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   return e != cudaSuccess ? e : launch_pdl(k, grid, dim3(kEditThreads), smem, st, a);

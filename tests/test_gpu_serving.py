@@ -2,8 +2,8 @@
 (oracle/serving.py).
 
 Tolerance of an edited logit. The kernel computes
-z = fl(fl(fl(x / r) - f c) - p) + bias in fp32. Each of its at most 4 + n_b
-operations (n_b bias entries of one token, 8 at most here) rounds a value no
+z = x fl(1 / r) - (f c + p) + bias in fp32. Each of its at most 5 + n_b
+operations (n_b bias entries of one token, 7 at most here) rounds a value no
 larger than S = |x / r or x r| + |f| c + |p| + sum |bias|, by 2^-24 of it; the
 parameters are the same fp32 numbers on both sides. So |z_gpu - z| <= E =
 12 * 2^-24 * S, and the final rounding adds half a step of the type, 2^-8
