@@ -23,14 +23,14 @@ namespace specv {
 #ifndef MINB
 #define MINB 2
 #endif
-#ifndef SPI
-#define SPI 4
+#ifndef SPX
+#define SPX 4
 #endif
-#ifndef SPO
-#define SPO 1
+#ifndef BATCH
+#define BATCH 8
 #endif
 #ifndef WANT
-#define WANT 4
+#define WANT 3
 #endif
 constexpr int kChunk = 1024;  // tokens of one warp's step over a row: 32 words of a bit table
 constexpr int kEditThreads = 512;
@@ -129,11 +129,17 @@ __device__ __forceinline__ void stream_chunk(const char* src, char* dst, int spa
     }
     return;
   }
+  if (INPLACE && __all_sync(0xffffffffu, allow == 0xffffffffu)) return;
   const int head = min(span, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / es);
   const int nvec = (span - head) / E;
   src += (head + lane * E) * es;  // the lane's first vector
   dst += (head + lane * E) * es;
   constexpr int kStep = 32 * 16, kFly = 4;  // bytes from vector to vector; vectors in flight per lane
+  if (INPLACE && head == 0 && span == kChunk && __all_sync(0xffffffffu, allow == 0u)) {
+#pragma unroll
+    for (int t = 0; t < NV; ++t) *reinterpret_cast<uint4*>(dst + t * kStep) = neg_inf16<DT>();
+    return;
+  }
   uint4 v[kFly];
   if constexpr (!INPLACE) {
 #pragma unroll
@@ -236,38 +242,43 @@ __device__ __forceinline__ int64_t row_byte(const RulesArgs& a, const Request& r
   return row * a.V * Elem<DT>::kBytes;
 }
 
-// Block (x, b, z): 8192 tokens, 1024 to a warp, of `per` rows of request b.
+// Block (x, b, q): chunks x * per ... of row q of request b, one after the
+// other to its warps, the masks of the next four chunks on their way.
 template <int DT, bool INPLACE>
 __global__ void __launch_bounds__(kThreads, 6) k_rules_stream(const RulesArgs a) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kChunk;
   const Request r = load_request(a, b);
   if (r.flag) {
     if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(a.status, r.flag);
     return;
   }
-  const int q0 = blockIdx.z * a.per, nq = min(a.K * r.nrow - q0, a.per);
-  if (t0 >= a.V || nq <= 0 || (INPLACE && r.m < 0)) return;
-  const int span = static_cast<int>(min(static_cast<int64_t>(kChunk), a.V - t0));
-  const int64_t W = (a.V + 31) / 32, w = t0 / 32 + lane, pitch = a.V * Elem<DT>::kBytes;
-  const bool masked = r.m >= 0 && w < W;
+  const int q = blockIdx.z;
+  if (q >= a.K * r.nrow || (INPLACE && r.m < 0)) return;
   int i;
-  int64_t off = row_byte<DT>(a, r, b, q0, i) + t0 * Elem<DT>::kBytes;
-  const uint32_t* mask = a.mask + static_cast<int64_t>(r.m) * a.mask_len * W + w;
-  uint32_t next = masked ? mask[i * W] : 0xffffffffu;
+  const int64_t row = row_byte<DT>(a, r, b, q, i);
+  const int chunks = static_cast<int>((a.V + kChunk - 1) / kChunk);
+  const int end = min(chunks, (static_cast<int>(blockIdx.x) + 1) * a.per);
+  int c = blockIdx.x * a.per + (threadIdx.x >> 5);
+  const int W = static_cast<int>((a.V + 31) / 32);
+  const uint32_t* mask = a.mask + (static_cast<int64_t>(r.m) * a.mask_len + i) * W;
+  auto allowed = [&](int chunk) {
+    const int w = chunk * 32 + lane;
+    return r.m >= 0 && chunk < end && w < W ? mask[w] : 0xffffffffu;
+  };
+  uint32_t allow[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) allow[k] = allowed(c + k * kWarps);
 #pragma unroll 1
-  for (int k = 0; k < nq; ++k) {  // the next row's mask is on its way while this row is written
-    const uint32_t allow = next;
-    const int64_t at = off;
-    off += pitch;
-    if (++i == r.nrow) {  // the next branch
-      i = 0;
-      off += (a.rows - r.nrow) * pitch;
-    }
-    if (masked && k + 1 < nq) next = mask[i * W];
-    stream_chunk<DT, INPLACE>(a.x + at, a.out + at, span, allow);
+  for (; c < end; c += kWarps) {
+    const int64_t t0 = static_cast<int64_t>(c) * kChunk, off = row + t0 * Elem<DT>::kBytes;
+    const uint32_t now = allow[0];
+    allow[0] = allow[1];
+    allow[1] = allow[2];
+    allow[2] = allow[3];
+    allow[3] = allowed(c + 4 * kWarps);
+    stream_chunk<DT, INPLACE>(a.x + off, a.out + off, static_cast<int>(min(static_cast<int64_t>(kChunk), a.V - t0)), now);
   }
 }
 
@@ -278,7 +289,7 @@ struct Special {
   float* add;         // bias value; an owner's: the sum of its token's
   uint32_t* drafted;  // an owner's: bit k, drafted at position k
   int* count;         // an owner's: its count, -1 when not seen
-  int* twice;         // tokens that more than one entry names
+  int* twice;         // entries whose token another one had named already
   uint16_t* owner;    // entries that speak for their token
 };
 constexpr int kSpecialBytes = 5 * 4 + 2;
@@ -304,7 +315,7 @@ __device__ __forceinline__ Special carve_special(char* base, int n) {
 // row to row or has a sum in it, come first in the list and go a slower way.
 template <int DT>
 __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesArgs a) {
-  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 8;  // WPT words of the bit table per thread
+  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = BATCH;  // WPT words of the bit table per thread
   constexpr int es = Elem<DT>::kBytes;
   extern __shared__ __align__(16) char s_dyn[];
   uint32_t* s_word = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] the tile's seen bits
@@ -314,34 +325,51 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
   const Special sp = carve_special(reinterpret_cast<char*>(s_minus + kListMax), a.special);
   __shared__ int64_t s_off[kRowsMax];     // first byte of a row
   __shared__ int16_t s_pos[kRowsMax];
-  __shared__ int s_n, s_nt, s_no;
+  __shared__ int s_rank[NT], s_warp[NT / 32];
+  __shared__ int s_nt, s_no;
   const int tid = threadIdx.x, lane = tid & 31;
   const int b = blockIdx.x;
   const int64_t V = a.V, W = (V + 31) / 32;
   const bool special = a.L + a.h.n_bias > 0;
   for (int w = tid; special && w < WPT * NT; w += NT) s_claim[w] = 0u;
-  if (tid == 0) s_n = s_nt = s_no = 0;
+  if (tid == 0) s_nt = s_no = 0;
   pdl_wait();
   pdl_trigger();
 
   const Request r = load_request(a, b);
+  const int seat = r.seat, m = r.m, n_bias = r.sat ? a.h.n_bias : 0;
+  const uint32_t* seen = a.h.seen + seat * W;
+  const int32_t* counts = a.h.counts + seat * V;
+  int entry = -1;  // a special entry: token and bias
+  float value = 0.f;
+  auto load_entry = [&](int e) {
+    entry = -1;
+    value = 0.f;
+    if (e < 32) {
+      if (e < min(r.ell, a.L)) entry = a.tokens[static_cast<int64_t>(b) * a.L + e];
+    } else if (e < 32 + n_bias) {
+      entry = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
+      value = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
+    }
+  };
+  // the first tile's words and the first entries need the seat alone: they are asked for before the penalties are known
+  uint32_t word[WPT];
+#pragma unroll
+  for (int k = 0; k < WPT; ++k)
+    word[k] = r.sat && (tid + k * NT) * 32 < V ? seen[tid + k * NT] : 0u;
+  load_entry(tid);
   if (r.flag) {
     if (blockIdx.y == 0 && tid == 0) atomicOr(a.status, r.flag);
     return;
   }
   const bool pen = r.pen;
-  const int seat = r.seat, m = r.m;
   // x / r as x times the rounded 1 / r: one more rounding of 2^-24, for a division less per element
   const float rep = r.rep, inv = 1.f / r.rep, freq = r.freq, pres = r.pres;
-  const int n_bias = r.sat ? a.h.n_bias : 0, n_tok = pen ? r.ell : 0;
+  const bool counted = pen && (freq != 0.f || pres != 0.f);  // the repetition penalty needs the seen bits alone
+  const int n_tok = pen ? r.ell : 0;
   const int q0 = blockIdx.y * a.per, nq = min(a.K * r.nrow, q0 + a.per) - q0;
-  if (blockIdx.y == 0 && tid < n_tok) {
-    const int x = a.tokens[static_cast<int64_t>(b) * a.L + tid];
-    if (x < 0 || x >= V) atomicOr(a.status, kFlagTokenRange);
-  }
+  if (blockIdx.y == 0 && tid < n_tok && (entry < 0 || entry >= V)) atomicOr(a.status, kFlagTokenRange);
   if (nq <= 0 || (!pen && n_bias == 0)) return;
-  const uint32_t* seen = a.h.seen + seat * W;
-  const int32_t* counts = a.h.counts + seat * V;
   const uint32_t* mask = a.mask + (m >= 0 ? static_cast<int64_t>(m) * a.mask_len * W : 0);
   for (int q = tid; q < nq; q += NT) {
     int i;
@@ -355,34 +383,21 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
     if (t0) {  // a further tile: the last one's shared memory is free
       __syncthreads();
       for (int w = tid; special && w < WPT * NT; w += NT) s_claim[w] = 0u;
-      if (tid == 0) s_n = s_nt = s_no = 0;
+      if (tid == 0) s_nt = s_no = 0;
     }
-    {
-      uint32_t word[WPT];
+    if (t0) {
 #pragma unroll
-      for (int k = 0; k < WPT; ++k) word[k] = pen && (tid + k * NT) * 32 < span ? seen[w0 + tid + k * NT] : 0u;
-#pragma unroll
-      for (int k = 0; k < WPT; ++k) s_word[tid + k * NT] = word[k];
+      for (int k = 0; k < WPT; ++k)
+        word[k] = (tid + k * NT) * 32 < span ? seen[w0 + tid + k * NT] : 0u;
     }
-    int64_t entry = -1;  // special entry tid, loaded together with the words
-    float value = 0.f;
-    auto load_entry = [&](int e) {
-      entry = -1;
-      value = 0.f;
-      if (e < 32) {
-        if (e < n_tok) entry = a.tokens[static_cast<int64_t>(b) * a.L + e];
-      } else if (e < 32 + n_bias) {
-        entry = a.h.bias_tokens[static_cast<int64_t>(seat) * n_bias + e - 32];
-        value = a.h.bias_values[static_cast<int64_t>(seat) * n_bias + e - 32];
-      }
-    };
-    load_entry(tid);
-    __syncthreads();  // s_claim, s_n, s_nt, s_no, s_off, s_pos
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) s_word[tid + k * NT] = pen ? word[k] : 0u;
+    __syncthreads();  // s_claim, s_word, s_nt, s_no, s_off, s_pos
     if (n_tok + n_bias > 0) {
       uint32_t mine = 0u;  // entries this thread was the first to name
       for (int e = tid, j = 0; e < 32 + n_bias; e += NT, ++j) {
-        if (j) load_entry(e);
-        const int64_t x = entry;
+        if (j || t0) load_entry(e);
+        const int64_t x = e < 32 && e >= n_tok ? -1 : entry;
         const float add = value;
         if (e >= 32 && x >= V && blockIdx.y == 0 && t0 == 0) atomicOr(a.status, kFlagTokenRange);
         const bool in = x >= t0 && x < t0 + span;
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
         sp.add[e] = add;
         if (in) {
           const uint32_t bit = 1u << (v & 31);
-          if (atomicOr(&s_claim[v >> 5], bit) & bit) sp.twice[atomicAdd(&s_nt, 1)] = v;
+          if (atomicOr(&s_claim[v >> 5], bit) & bit) sp.twice[atomicAdd(&s_nt, 1)] = e;
           else mine |= 1u << j;
         }
       }
@@ -404,30 +419,37 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
         const int v = sp.v[e];
         uint32_t drafted = e < 32 ? 1u << e : 0u;
         const uint32_t bits = pen ? seen[w0 + (v >> 5)] : 0u;
-        const int stored = pen ? counts[t0 + v] : 0;  // on its way beside the bits: 0 where the bit is not set
+        const int stored = counted ? counts[t0 + v] : 0;  // on its way beside the bits: 0 where the bit is not set
         const int count = bits >> (v & 31) & 1 ? stored : -1;
-        bool more = false;
-        for (int k = 0; k < nt; ++k) more |= sp.twice[k] == v;
-        if (more) {
-          float add = 0.f;
-          for (int k = 0; k < n_tok; ++k) drafted |= (sp.v[k] == v ? 1u : 0u) << k;
+        int biases = e >= 32;
+        float add = sp.add[e];
+        for (int k = 0; k < nt; ++k) {
+          const int o = sp.twice[k];
+          if (sp.v[o] != v) continue;
+          if (o < 32) {
+            drafted |= 1u << o;
+          } else {
+            add = biases++ ? add + sp.add[o] : sp.add[o];
+          }
+        }
+        if (biases > 2) {  // of two, the order does not matter
+          add = 0.f;
           for (int k = 32; k < 32 + n_bias; ++k)
             if (sp.v[k] == v) add += sp.add[k];
-          sp.add[e] = add;  // no other thread reads the entries of this token
         }
+        sp.add[e] = add;  // no other thread reads the entries of this token
         sp.drafted[e] = drafted;
         sp.count[e] = count;
         sp.owner[atomicAdd(&s_no, 1)] = static_cast<uint16_t>(e);
       }
     }
+    // seen tokens by rank: thread t counts words t * WPT ...; s_rank[t] is the rank of its first token
     int mine = 0;
-#pragma unroll 1
-    for (int w = tid; w < WPT * NT; w += NT) {
-      const int left = span - w * 32;
-      if (left <= 0) break;
-      uint32_t bits = s_word[w];
+    for (int k = 0; k < WPT; ++k) {
+      const int w = tid * WPT + k, left = span - w * 32;
+      uint32_t bits = left > 0 ? s_word[w] : 0u;
       if (special) bits &= ~s_claim[w];
-      if (left < 32) bits &= (1u << left) - 1u;
+      if (left < 32 && left > 0) bits &= (1u << left) - 1u;
       s_word[w] = bits;
       mine += __popc(bits);
     }
@@ -437,25 +459,55 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
       const int t = __shfl_up_sync(0xffffffffu, rank, o);
       if (lane >= o) rank += t;
     }
-    int base = 0;
-    if (lane == 31 && rank) base = atomicAdd(&s_n, rank);  // the warps' order is free: tokens are independent
-    rank = __shfl_sync(0xffffffffu, base, 31) + rank - mine;
+    if (lane == 31) s_warp[tid >> 5] = rank;
+    __syncthreads();  // s_warp, s_no
+    {
+      const int sum = lane < NT / 32 ? s_warp[lane] : 0;
+      int all = sum;
+#pragma unroll
+      for (int o = 1; o < NT / 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += t;
+      }
+      rank += __shfl_sync(0xffffffffu, all - sum, tid >> 5);
+      s_rank[tid] = rank - mine;
+      mine = __shfl_sync(0xffffffffu, all, NT / 32 - 1);
+    }
+    __syncthreads();  // s_rank, s_word
 
     // named tokens x rows; the list in rounds of kListMax (one, unless the history is very long)
-    __syncthreads();  // s_n, s_no
-    const int n = s_n, no = s_no;
+    const int n = mine, no = s_no;
     for (int l0 = 0; l0 == 0 || l0 < n; l0 += kListMax) {
       const int ln = min(kListMax, n - l0);
       if (ln == 0 && no == 0) break;
       if (l0) __syncthreads();
-      if (ln > 0) {
-        int at = rank - l0;
-#pragma unroll 1
-        for (int w = tid; w * 32 < span; w += NT)
-          for (uint32_t left = s_word[w]; left; left &= left - 1, ++at)
-            if (at >= 0 && at < kListMax) s_list[at] = w * 32 + __ffs(left) - 1;
-        __syncthreads();
+      // the token of rank j: a search over the threads' ranks, then over the thread's words, then over the word's bits
+#pragma unroll 2
+      for (int e = tid; e < ln; e += NT) {
+        const int j = l0 + e;
+        int lo = 0;
+#pragma unroll
+        for (int step = NT / 2; step > 0; step >>= 1)
+          if (s_rank[lo + step] <= j) lo += step;
+        int left = j - s_rank[lo], w = lo * WPT, c = __popc(s_word[w]);
+        while (left >= c) {
+          left -= c;
+          c = __popc(s_word[++w]);
+        }
+        uint32_t bits = s_word[w];
+        int at = 0;
+#pragma unroll
+        for (int half = 16; half > 0; half >>= 1) {
+          const int low = __popc(bits & ((1u << half) - 1u));
+          if (left >= low) {
+            left -= low;
+            at += half;
+            bits >>= half;
+          }
+        }
+        s_list[e] = w * 32 + at;
       }
+      if (ln > 0) __syncthreads();
       const char* x = a.x + t0 * es;
       char* y = a.out + t0 * es;
       const int dq = ln ? NT / ln : 0, de = NT - dq * ln;  // a step of NT elements
@@ -498,7 +550,7 @@ __global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesAr
           for (int j = tid; j < ln; j += 4 * NT) {
             int c[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] = j + k * NT < ln ? counts[t0 + s_list[j + k * NT]] : 0;
+            for (int k = 0; k < 4; ++k) c[k] = counted && j + k * NT < ln ? counts[t0 + s_list[j + k * NT]] : 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (j + k * NT < ln) s_minus[j + k * NT] = freq * static_cast<float>(c[k]) + (c[k] > 0 ? pres : 0.f);
@@ -526,10 +578,13 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   const int most = a.K * a.rows;
   const bool inplace = a.x == a.out;
   if (!inplace || a.mask) {
-    const int64_t x = (a.V + kWarps * kChunk - 1) / (kWarps * kChunk);
-    a.per = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(inplace ? SPI : SPO, x * a.B * most / (148 * 6))));
-    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.B),
-                    static_cast<unsigned>((most + a.per - 1) / a.per));
+    // a row is cut until the grid has SPX blocks for each of the GPU's slots, 8 chunks (one per warp) at least;
+    // copies, which have their data to wait for, into those
+    const int64_t chunks = (a.V + kChunk - 1) / kChunk, rows = static_cast<int64_t>(a.B) * most;
+    const int64_t cut = std::max<int64_t>(1, std::min<int64_t>((chunks + kWarps - 1) / kWarps, 148 * 6 * SPX / rows));
+    a.per = inplace ? static_cast<int>((chunks + cut - 1) / cut) : kWarps;
+    const dim3 grid(static_cast<unsigned>((chunks + a.per - 1) / a.per), static_cast<unsigned>(a.B),
+                    static_cast<unsigned>(most));
     void (*k)(RulesArgs) = dtype == 0 ? (inplace ? k_rules_stream<0, true> : k_rules_stream<0, false>)
                                       : (inplace ? k_rules_stream<1, true> : k_rules_stream<1, false>);
     const cudaError_t e = launch_pdl(k, grid, dim3(kThreads), 0, st, a);
