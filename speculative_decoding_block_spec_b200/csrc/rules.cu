@@ -20,18 +20,6 @@
 
 namespace specv {
 
-#ifndef MINB
-#define MINB 2
-#endif
-#ifndef SPX
-#define SPX 4
-#endif
-#ifndef BATCH
-#define BATCH 8
-#endif
-#ifndef WANT
-#define WANT 3
-#endif
 constexpr int kChunk = 1024;  // tokens of one warp's step over a row: 32 words of a bit table
 constexpr int kEditThreads = 512;
 constexpr int kEditTile = 10 * 32 * kEditThreads;  // tokens of the edit kernel's tile: 163,840
@@ -314,8 +302,8 @@ __device__ __forceinline__ Special carve_special(char* base, int n) {
 // need their count alone; drafted and biased ones, whose value differs from
 // row to row or has a sum in it, come first in the list and go a slower way.
 template <int DT>
-__global__ void __launch_bounds__(kEditThreads, MINB) k_rules_edit(const RulesArgs a) {
-  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = BATCH;  // WPT words of the bit table per thread
+__global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs a) {
+  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 8;  // WPT words of the bit table per thread
   constexpr int es = Elem<DT>::kBytes;
   extern __shared__ __align__(16) char s_dyn[];
   uint32_t* s_word = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] the tile's seen bits
@@ -578,10 +566,10 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   const int most = a.K * a.rows;
   const bool inplace = a.x == a.out;
   if (!inplace || a.mask) {
-    // a row is cut until the grid has SPX blocks for each of the GPU's slots, 8 chunks (one per warp) at least;
+    // a row is cut until the grid has 8 blocks for each of the GPU's 148 x 6 slots, 8 chunks (one per warp) at least;
     // copies, which have their data to wait for, into those
     const int64_t chunks = (a.V + kChunk - 1) / kChunk, rows = static_cast<int64_t>(a.B) * most;
-    const int64_t cut = std::max<int64_t>(1, std::min<int64_t>((chunks + kWarps - 1) / kWarps, 148 * 6 * SPX / rows));
+    const int64_t cut = std::max<int64_t>(1, std::min<int64_t>((chunks + kWarps - 1) / kWarps, 148 * 48 / rows));
     a.per = inplace ? static_cast<int>((chunks + cut - 1) / cut) : kWarps;
     const dim3 grid(static_cast<unsigned>((chunks + a.per - 1) / a.per), static_cast<unsigned>(a.B),
                     static_cast<unsigned>(most));
@@ -591,7 +579,7 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
     if (e != cudaSuccess) return e;
   }
   if (!a.h.counts) return cudaSuccess;
-  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * WANT / a.B)));
+  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 3 / a.B)));
   a.per = (most + z - 1) / z;
   a.special = 32 + a.h.n_bias;
   const dim3 grid(static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));

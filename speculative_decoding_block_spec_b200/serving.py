@@ -14,7 +14,9 @@ import ctypes
 
 import torch
 
-_I32, _F32 = torch.int32, torch.float32
+from . import SpecError, Workspace, _dtype_code, lib
+
+_I32, _F32, _I64 = torch.int32, torch.float32, torch.int64
 
 
 class _CHistory(ctypes.Structure):
@@ -29,24 +31,21 @@ class _CPages(ctypes.Structure):
 
 
 def _check(t, name, dtype, shape, device=None):
-    """Raises unless t is a contiguous tensor of `dtype` and `shape` (None: any size) on `device`; returns its
-    address. Shapes come first, so a mis-sized tensor is named even where there is no CUDA device."""
+    """Raises unless t is a contiguous tensor of `dtype` and `shape` (None: any size) on device number `device`
+    (-1: host); returns its address. Shapes come first, so a mis-sized tensor is named even where there is no CUDA
+    device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
     s = t.shape
-    if len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape)):
+    if s != shape and (len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape))):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(s), tuple("*" if w is None else w for w in shape)))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, device))
+    if device is not None and t.get_device() != device:
+        raise ValueError("%s is on %s, the call's other tensors on device %d" % (name, t.device, device))
     return t.data_ptr()
-
-
-def _opt(t, name, dtype, shape, device):
-    return None if t is None else _check(t, name, dtype, shape, device)
 
 
 class History:
@@ -62,11 +61,11 @@ class History:
         c = _CHistory()
         c.counts = _check(counts, "counts", _I32, (None, None))
         seats, V = counts.shape
-        dev = counts.device
+        dev = counts.get_device()
         c.seen = _check(seen, "seen", _I32, (seats, (V + 31) // 32), dev)
-        c.repetition = _opt(repetition, "repetition", _F32, (seats,), dev)
-        c.frequency = _opt(frequency, "frequency", _F32, (seats,), dev)
-        c.presence = _opt(presence, "presence", _F32, (seats,), dev)
+        c.repetition = None if repetition is None else _check(repetition, "repetition", _F32, (seats,), dev)
+        c.frequency = None if frequency is None else _check(frequency, "frequency", _F32, (seats,), dev)
+        c.presence = None if presence is None else _check(presence, "presence", _F32, (seats,), dev)
         if (bias_tokens is None) != (bias_values is None):
             raise ValueError("bias_tokens and bias_values go together")
         n = 0
@@ -75,7 +74,7 @@ class History:
             n = bias_tokens.shape[1]
             c.bias_values = _check(bias_values, "bias_values", _F32, (seats, n), dev)
         c.n_bias, c.seats, c.V = n, seats, V
-        self._c, self._ref, self.device, self.seats, self.V = c, ctypes.byref(c), dev, seats, V
+        self._c, self._ref, self._dev, self.seats, self.V = c, ctypes.byref(c), dev, seats, V
         self._tensors = (counts, seen, repetition, frequency, presence, bias_tokens, bias_values)
 
     @classmethod
@@ -105,7 +104,7 @@ class KvPages:
     def __init__(self, page_table, owned, free_pages, free_count, page_size):
         c = _CPages()
         c.page_table = _check(page_table, "page_table", _I32, (None, None))
-        dev = page_table.device
+        dev = page_table.get_device()
         c.seats, c.max_pages = page_table.shape
         c.owned = _check(owned, "owned", _I32, (c.seats,), dev)
         c.free_pages = _check(free_pages, "free_pages", _I32, (None,), dev)
@@ -113,7 +112,7 @@ class KvPages:
         if not 1 <= int(page_size) <= 0x7fffffff:
             raise ValueError("page_size must be positive")
         c.n_pages, c.page_size = free_pages.shape[0], int(page_size)
-        self._c, self._ref, self.device, self.page_size = c, ctypes.byref(c), dev, int(page_size)
+        self._c, self._ref, self._dev, self.page_size = c, ctypes.byref(c), dev, int(page_size)
         self.seats, self.max_pages, self.n_pages = c.seats, c.max_pages, c.n_pages
         self._tensors = (page_table, owned, free_pages, free_count)
 
@@ -131,33 +130,37 @@ class KvPages:
     free_count = property(lambda self: self._tensors[3])
 
 
-def _workspace(workspace, nbytes, device):
-    from . import Workspace
-    if workspace is None:
-        return Workspace(nbytes, device)
-    if workspace.buf.device != device:
-        raise ValueError("workspace is on %s, the call's other tensors on %s" % (workspace.buf.device, device))
-    return workspace
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _launch(device, name, *args):
-    """The library call on the current stream of `device`, with that device current."""
-    from . import _call
-    if device.type != "cuda":
+# the same handle without a Stream object made for it, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _launch(device, workspace, nbytes, name, *args):
+    """The library call on the current stream of device number `device`, with that device current. Without a
+    workspace, the call gets one of its own."""
+    if device < 0:
         raise TypeError("%s: tensors must be CUDA tensors" % name)
-    if torch.cuda.current_device() != device.index:
+    if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
-            return _call(name, *args, torch.cuda.current_stream(device).cuda_stream)
-    return _call(name, *args, torch.cuda.current_stream(device).cuda_stream)
+            return _launch(device, workspace, nbytes, name, *args)
+    if workspace is None:
+        workspace = Workspace(nbytes, torch.device("cuda", device))
+    buf = workspace.buf
+    if buf.get_device() != device:
+        raise ValueError("workspace is on %s, the call's other tensors on device %d" % (buf.device, device))
+    st = getattr(lib(), name)(*args, buf.data_ptr(), buf.numel(), _raw_stream(device))
+    if st != 0:
+        raise SpecError(name, st)
 
 
 def rules_workspace_size(B):
-    from . import lib
     return int(lib().spec_rules_workspace_size(B))
 
 
 def kv_workspace_size(B):
-    from . import lib
     return int(lib().spec_kv_workspace_size(B))
 
 
@@ -176,10 +179,10 @@ def spec_logit_rules(logits, history=None, *, seats=None, draft_tokens=None, ver
             token v is allowed; mask_rows [B] int32, the request's mask or
             negative (None: mask b).
     out     None: in place. Returns the edited rows."""
-    from . import _dtype_code
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a tensor")
-    dev, V, K = logits.device, logits.shape[-1] if logits.dim() else 0, 1
+    dev, shape, K = logits.get_device(), logits.shape, 1
+    V = shape[-1] if shape else 0
     L = None
     if draft_tokens is not None:
         if draft_tokens.dim() != 2:
@@ -207,17 +210,17 @@ def spec_logit_rules(logits, history=None, *, seats=None, draft_tokens=None, ver
             raise ValueError("logits has shape %s, expected %d requests of %d (draft) or %d (target) rows"
                              % (tuple(logits.shape), B, L, L + 1))
     dt = _dtype_code(logits)
-    shape = tuple(logits.shape)
     xp = _check(logits, "logits", logits.dtype, shape, dev)
     op = xp if out is None else _check(out, "out", logits.dtype, shape, dev)
-    tp = _opt(draft_tokens, "draft_tokens", _I32, (B, L), dev)
-    rp = _opt(target_row_off, "target_row_off", _I32, (None,), dev)
-    vp = _opt(verify_len, "verify_len", _I32, (B,), dev)
-    sp = _opt(seats, "seats", _I32, (B,), dev)
+    tp = None if draft_tokens is None else _check(draft_tokens, "draft_tokens", _I32, (B, L), dev)
+    rp = None if target_row_off is None else _check(target_row_off, "target_row_off", _I32, (None,), dev)
+    vp = None if verify_len is None else _check(verify_len, "verify_len", _I32, (B,), dev)
+    sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
     hp = None
     if history is not None:
-        if history.device != dev or history.V != V:
-            raise ValueError("history holds V = %d on %s, logits V = %d on %s" % (history.V, history.device, V, dev))
+        if history._dev != dev or history.V != V:
+            raise ValueError("history holds V = %d on device %d, logits V = %d on device %d"
+                             % (history.V, history._dev, V, dev))
         if seats is None and B > history.seats:
             raise ValueError("seats: %d requests for %d seats" % (B, history.seats))
         hp = history._ref
@@ -228,15 +231,14 @@ def spec_logit_rules(logits, history=None, *, seats=None, draft_tokens=None, ver
         n_masks, mask_len = mask.shape[0], mask.shape[1]
         if mask_len < rows or n_masks < 1:
             raise ValueError("mask has shape %s, expected at least %d rows a mask" % (tuple(mask.shape), rows))
-        np_ = _opt(mask_rows, "mask_rows", _I32, (B,), dev)
+        np_ = None if mask_rows is None else _check(mask_rows, "mask_rows", _I32, (B,), dev)
         if mask_rows is None and n_masks < B:
             raise ValueError("mask_rows: %d requests for %d masks" % (B, n_masks))
     elif mask_rows is not None:
         raise ValueError("mask_rows needs mask")
-    ws = _workspace(workspace, 256, dev)
     n_rows = shape[0] if target_row_off is not None else B * K * rows
-    _launch(dev, "spec_logit_rules", xp, op, dt, rp, n_rows, B, K, rows, L, V, tp, vp, hp, sp, mp, n_masks, mask_len,
-            np_, ws.ptr(), ws.nbytes)
+    _launch(dev, workspace, 256, "spec_logit_rules", xp, op, dt, rp, n_rows, B, K, rows, L, V, tp, vp, hp, sp, mp,
+            n_masks, mask_len, np_)
     return logits if out is None else out
 
 
@@ -244,7 +246,7 @@ def spec_history_add(history, tokens, *, seats=None, offsets=None, output=True, 
     """Tokens enter the history of their requests' seats: tokens [B, M] int32
     (negative: padding; the out_tokens of a verify call), or [N] with offsets
     [B + 1] int32. output: generated tokens (counted), else prompt tokens."""
-    dev = history.device
+    dev = history._dev
     if offsets is None:
         tp = _check(tokens, "tokens", _I32, (None, None), dev)
         B = tokens.shape[0]
@@ -253,20 +255,17 @@ def spec_history_add(history, tokens, *, seats=None, offsets=None, output=True, 
         tp = _check(tokens, "tokens", _I32, (None,), dev)
         op = _check(offsets, "offsets", _I32, (None,), dev)
         B = offsets.shape[0] - 1
-    sp = _opt(seats, "seats", _I32, (B,), dev)
+    sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
     if seats is None and B > history.seats:
         raise ValueError("seats: %d requests for %d seats" % (B, history.seats))
-    ws = _workspace(workspace, 256, dev)
-    _launch(dev, "spec_history_add", history._ref, sp, B, tp, tokens.numel(), op, 1 if output else 0, ws.ptr(),
-            ws.nbytes)
+    _launch(dev, workspace, 256, "spec_history_add", history._ref, sp, B, tp, tokens.numel(), op, 1 if output else 0)
 
 
 def spec_history_clear(history, seats, *, workspace=None):
     """Empties the history of seats [B] int32 (negative: skipped)."""
-    dev = history.device
+    dev = history._dev
     sp = _check(seats, "seats", _I32, (None,), dev)
-    ws = _workspace(workspace, 256, dev)
-    _launch(dev, "spec_history_clear", history._ref, sp, seats.shape[0], ws.ptr(), ws.nbytes)
+    _launch(dev, workspace, 256, "spec_history_clear", history._ref, sp, seats.shape[0])
 
 
 def spec_kv_map(pages, ctx_len, offsets, n_tokens, *, seats=None, block_table=None, out=None, workspace=None):
@@ -275,32 +274,31 @@ def spec_kv_map(pages, ctx_len, offsets, n_tokens, *, seats=None, block_table=No
     behind the ctx_len [B] int32 tokens of each request. n_tokens: capacity of
     the outputs. block_table [B, max_pages] int32 (None: not written).
     Returns (kv_slots [n_tokens] int64, positions [n_tokens] int32, seq_len [B] int32)."""
-    dev = pages.device
+    dev = pages._dev
     cp = _check(ctx_len, "ctx_len", _I32, (None,), dev)
     B, N = ctx_len.shape[0], int(n_tokens)
     fp = _check(offsets, "offsets", _I32, (B + 1,), dev)
-    sp = _opt(seats, "seats", _I32, (B,), dev)
+    sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
     if seats is None and B > pages.seats:
         raise ValueError("seats: %d requests for %d seats" % (B, pages.seats))
-    bp = _opt(block_table, "block_table", _I32, (B, pages.max_pages), dev)
+    bp = None if block_table is None else _check(block_table, "block_table", _I32, (B, pages.max_pages), dev)
     if out is None:
-        out = (torch.empty(N, dtype=torch.int64, device=dev), torch.empty(N, dtype=_I32, device=dev),
-               torch.empty(B, dtype=_I32, device=dev))
+        on = ctx_len.device
+        out = (torch.empty(N, dtype=_I64, device=on), torch.empty(N, dtype=_I32, device=on),
+               torch.empty(B, dtype=_I32, device=on))
     slots, positions, seq_len = out
-    kp = _check(slots, "kv_slots", torch.int64, (N,), dev)
-    pp = _opt(positions, "positions", _I32, (N,), dev)
+    kp = _check(slots, "kv_slots", _I64, (N,), dev)
+    pp = None if positions is None else _check(positions, "positions", _I32, (N,), dev)
     qp = _check(seq_len, "seq_len", _I32, (B,), dev)
-    ws = _workspace(workspace, 512, dev)
-    _launch(dev, "spec_kv_map", pages._ref, sp, B, cp, fp, N, kp, pp, qp, bp, ws.ptr(), ws.nbytes)
+    _launch(dev, workspace, 512, "spec_kv_map", pages._ref, sp, B, cp, fp, N, kp, pp, qp, bp)
     return out
 
 
 def spec_kv_release(pages, seats, *, keep_len=None, workspace=None):
     """Requests in seats [B] int32 (negative: skipped) give back the pages
     behind their first keep_len [B] int32 tokens (None: all of them)."""
-    dev = pages.device
+    dev = pages._dev
     sp = _check(seats, "seats", _I32, (None,), dev)
     B = seats.shape[0]
-    kp = _opt(keep_len, "keep_len", _I32, (B,), dev)
-    ws = _workspace(workspace, 512, dev)
-    _launch(dev, "spec_kv_release", pages._ref, sp, B, kp, ws.ptr(), ws.nbytes)
+    kp = None if keep_len is None else _check(keep_len, "keep_len", _I32, (B,), dev)
+    _launch(dev, workspace, 512, "spec_kv_release", pages._ref, sp, B, kp)
