@@ -596,58 +596,90 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
 //  offsets != NULL: tokens[offsets[b] .. offsets[b + 1]) belong to request b.
 //  offsets == NULL: tokens is [B, width].
 // Negative tokens are padding.
+//
+// A block takes 1024 tokens. A prompt names a few low ids again and again (3
+// in 10 tokens of a Zipf vocabulary of 152 K fall into one word of the
+// bits), and atomics on one address queue up: a block whose tokens belong to
+// one request first collects the bits of the ids below kHot in shared memory
+// and then writes each word once. 32 prompts of up to 8192 tokens, with
+// clearing their seats: 10.9 us by global atomics alone, 8.9 us so.
+constexpr int kAddTokens = 4;     // per thread
+constexpr int kHot = 32 * 2 * kThreads;
+
 __global__ void __launch_bounds__(kThreads) k_history_add(const spec_history h, const int32_t* __restrict__ seats,
                                                           int B, const int32_t* __restrict__ tokens, int64_t n,
                                                           const int32_t* __restrict__ offsets, int width, int output,
                                                           int* status) {
   extern __shared__ int s_off[];  // [B + 1]
+  __shared__ uint32_t s_hot[kHot / 32];
   __shared__ int s_bad;
+  const int tid = threadIdx.x;
+  if (tid == 0) s_bad = 0;
+  for (int w = tid; offsets && w < kHot / 32; w += kThreads) s_hot[w] = 0u;
   pdl_wait();
   pdl_trigger();
+  const int per = offsets ? kAddTokens : 1;  // a step's tokens are few: one to a thread
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kThreads * per;
+  int x[kAddTokens];
+#pragma unroll
+  for (int k = 0; k < kAddTokens; ++k) {
+    const int64_t t = t0 + tid + k * kThreads;
+    x[k] = k < per && t < n ? tokens[t] : -1;
+  }
   if (offsets) {
-    if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
-    for (int b = threadIdx.x; b <= B; b += kThreads) {
+    for (int b = tid; b <= B; b += kThreads) {
       const int o = offsets[b];
       s_off[b] = o;
       if (o < 0 || o > n || (b > 0 && offsets[b - 1] > o)) s_bad = 1;
     }
     __syncthreads();
     if (s_bad) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, kFlagLengths);
+      if (blockIdx.x == 0 && tid == 0) atomicOr(status, kFlagLengths);
       return;
     }
   }
-  const int64_t W = (h.V + 31) / 32;
-  int flag = 0;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; t < n;
-       t += static_cast<int64_t>(gridDim.x) * kThreads) {
-    int b;
-    if (offsets) {
-      if (t < s_off[0] || t >= s_off[B]) continue;
-      int lo = 0, hi = B - 1;  // last request with offset <= t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_off[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      b = lo;
-    } else {
-      b = static_cast<int>(t / width);
+  auto request_of = [&](int64_t t) {
+    if (!offsets) return static_cast<int>(t / width);
+    int lo = 0, hi = B - 1;  // last request with offset <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_off[mid] <= t) lo = mid; else hi = mid - 1;
     }
+    return lo;
+  };
+  const int64_t W = (h.V + 31) / 32;
+  const int b0 = request_of(t0);
+  const bool whole = offsets && request_of(min(t0 + kThreads * kAddTokens, n) - 1) == b0;  // one request's block
+  int flag = 0;
+#pragma unroll
+  for (int k = 0; k < kAddTokens; ++k) {
+    const int64_t t = t0 + tid + k * kThreads;
+    if (x[k] < 0 || (offsets && (t < s_off[0] || t >= s_off[B]))) continue;
+    const int b = whole ? b0 : request_of(t);
     const int seat = seats ? seats[b] : b;
-    const int64_t x = tokens[t];
-    if (x < 0 || seat < 0) continue;
+    if (seat < 0) continue;
     if (seat >= h.seats) { flag |= kFlagIndex; continue; }
-    if (x >= h.V) { flag |= kFlagTokenRange; continue; }
-    atomicOr(h.seen + seat * W + (x >> 5), 1u << (x & 31));
-    if (output) atomicAdd(h.counts + seat * h.V + x, 1);
+    if (x[k] >= h.V) { flag |= kFlagTokenRange; continue; }
+    const uint32_t bit = 1u << (x[k] & 31);
+    if (whole && x[k] < kHot) {
+      if (!(s_hot[x[k] >> 5] & bit)) atomicOr(&s_hot[x[k] >> 5], bit);
+    } else {
+      atomicOr(h.seen + seat * W + (x[k] >> 5), bit);
+    }
+    if (output) atomicAdd(h.counts + seat * h.V + x[k], 1);
   }
   if (flag) atomicOr(status, flag);
+  if (!whole) return;
+  __syncthreads();
+  const int hot_seat = seats ? seats[b0] : b0;  // in range wherever a bit was collected
+  for (int w = tid; w < kHot / 32; w += kThreads)
+    if (s_hot[w]) atomicOr(h.seen + hot_seat * W + w, s_hot[w]);
 }
 
 cudaError_t launch_history_add(const spec_history& h, const int32_t* seats, int B, const int32_t* tokens, int64_t n,
                                const int32_t* offsets, int width, int output, int* status, cudaStream_t st) {
-  const int64_t blocks = std::min<int64_t>((n + kThreads - 1) / kThreads, 148 * 8);
+  const int64_t per = kThreads * (offsets ? kAddTokens : 1), blocks = (n + per - 1) / per;
   const size_t smem = offsets ? sizeof(int) * (B + 1) : 0;
   return launch_pdl(k_history_add, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, st, h, seats, B, tokens, n,
                     offsets, width, output, status);

@@ -357,6 +357,25 @@ def test_history_matches_the_definition(V, output):
     np.testing.assert_array_equal(h.seen.cpu().numpy().view(np.uint32), seen)
 
 
+@pytest.mark.parametrize("output", [True, False])
+def test_history_of_long_prompts(output):
+    """Blocks of tokens inside one request, across two, before the first and behind the last; low and high ids."""
+    g = np.random.default_rng(9)
+    V, S, B = 60000, 4, 5
+    seats = np.array([2, 9, 0, -1, 2], np.int32)
+    n = np.array([3000, 2500, 1024, 5000, 6000])
+    off = (np.concatenate([[0], np.cumsum(n)]) + 1500).astype(np.int32)
+    flat = (V ** g.random(off[-1] + 3000) - 1).astype(np.int32)
+    flat[1600], flat[off[2] + 7] = V, V + 5
+    h, ws = specv.History.empty(S, V), specv.Workspace(256)
+    counts, seen, f = plain.history_add(np.zeros((S, V), np.int32), np.zeros((S, V // 32), np.uint32), seats,
+                                        [flat[off[b]:off[b + 1]] for b in range(B)], output)
+    specv.spec_history_add(h, dev(flat), offsets=dev(off), seats=dev(seats), output=output, workspace=ws)
+    np.testing.assert_array_equal(h.counts.cpu().numpy(), counts)
+    np.testing.assert_array_equal(h.seen.cpu().numpy().view(np.uint32), seen)
+    assert ws.status() == f == specv.DEV_INDEX | specv.DEV_TOKEN_RANGE
+
+
 @pytest.mark.parametrize("off", [[0, 5, 4, 8], [-1, 2, 4, 8], [0, 2, 4, 9], [3, 2, 2, 2]])
 def test_history_refuses_bad_offsets(off):
     h, ws = specv.History.empty(3, 100), specv.Workspace(256)
