@@ -67,7 +67,7 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_DEV_VERIFY_LEN 4   /* verify_len[b] outside [0, L]: accept_len = -1 */
 #define SPEC_DEV_SCORES 8       /* a survival score outside [0, 1] or NaN */
 #define SPEC_DEV_INDEX 16       /* a seat, mask or row offset outside its table, or a seat named twice: request left out */
-#define SPEC_DEV_PARAM 32       /* a penalty that is not finite, or repetition <= 0: request left out */
+#define SPEC_DEV_PARAM 32       /* a penalty that is not finite, or a repetition penalty outside its range: request left out */
 #define SPEC_DEV_PAGES 64       /* no free pages, or more than a page-table row holds: request refused */
 #define SPEC_DEV_LENGTHS 128    /* offsets, a length or a page count that cannot be: request or call left out */
 
@@ -339,7 +339,7 @@ typedef struct {
   int32_t* counts;            /* [seats, V] how often the request's output holds the token */
   uint32_t* seen;             /* [seats, ceil(V/32)] bit v%32 of word v/32: the prompt or the output holds token v;
                                  set wherever counts is not 0 */
-  const float* repetition;    /* [seats] r > 0 (NULL: 1) */
+  const float* repetition;    /* [seats] r, 2^-100 ... 2^100 (NULL: 1) */
   const float* frequency;     /* [seats] f (NULL: 0) */
   const float* presence;      /* [seats] p (NULL: 0) */
   const int32_t* bias_tokens; /* [seats, n_bias] (NULL when n_bias == 0); negative: unused entry */
@@ -378,8 +378,8 @@ size_t spec_kv_workspace_size(int B);
  *   z     = known ? (x > 0 ? x / r : x * r) : x
  *   z     = z - f c(v) - (c(v) > 0 ? p : 0) + sum of the seat's bias values at v
  *   out   = z, or -inf where the mask's bit v is 0 (whatever x is there)
- * in fp32, rounded once. Entries of a bias list that name one token add up in
- * list order.
+ * in fp32 (x / r as x times the rounded 1 / r), rounded once. Entries of a
+ * bias list that name one token add up in list order.
  *   logits      [B, K, rows, V] of `dtype`, or packed target rows [n_rows, V]
  *               with row_off (K == 1): row (b, i) is row_off[b] + i.
  *   out         same layout; == logits edits in place (only the elements that
@@ -401,7 +401,7 @@ size_t spec_kv_workspace_size(int B);
  *               ignored. A row that allows nothing becomes -inf throughout,
  *               and verification reports it as SPEC_DEV_NONFINITE.
  * A request with verify_len outside [0, L], an index outside its table, rows
- * outside the buffer or a penalty that is no number is left out: its flag is
+ * outside the buffer or a penalty outside its range is left out: its flag is
  * raised (SPEC_DEV_VERIFY_LEN, _INDEX, _PARAM) and none of its rows written.
  * Requests of one call must not share rows (they may share seats and masks).
  *   workspace   >= spec_rules_workspace_size(B) bytes.
@@ -471,7 +471,7 @@ int spec_history_clear(const spec_history* history, const int32_t* seats, int B,
  * overflow leaves the whole call undone (SPEC_DEV_LENGTHS).
  *
  * Both: workspace >= spec_kv_workspace_size(B) bytes, 1 <= B <= SPEC_MAX_B,
- * B * max_pages < 2^31. One launch each; results are functions of the inputs
+ * max_pages <= 2^30, B * max_pages < 2^31. One launch each; results are functions of the inputs
  * alone. Calls on one spec_kv_pages must be in stream order.
  */
 int spec_kv_map(const spec_kv_pages* pages, const int32_t* seats, int B, const int32_t* ctx_len,

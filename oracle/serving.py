@@ -57,7 +57,7 @@ def logit_rules(x, B, K, rows, L, *, row_off=None, tokens=None, verify_len=None,
             r = 1.0 if repetition is None else float(repetition[seat])
             f = 0.0 if frequency is None else float(frequency[seat])
             p = 0.0 if presence is None else float(presence[seat])
-            if not (0 < r < np.inf and np.isfinite(f) and np.isfinite(p)):
+            if not (2.0 ** -100 <= r <= 2.0 ** 100 and np.isfinite(f) and np.isfinite(p)):
                 flags |= FLAG_PARAM
                 continue
         if row_off is not None and not (0 <= row_off[b] and row_off[b] + n <= n_rows):

@@ -341,7 +341,9 @@ namespace {
 cudaError_t launch_kv(void (*k)(KvArgs), const KvArgs& a, cudaStream_t st) {
   const size_t smem = kv_shared_bytes(a.B, a.p.seats);
   if (smem > 40 * 1024) {  // the static arrays take less than 8 KiB more
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // always the most that a call can need: another host thread may be between its own setting and launch
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kv_shared_bytes(SPEC_MAX_B, SPEC_MAX_SEATS)));
     if (e != cudaSuccess) return e;
   }
   const int64_t items = static_cast<int64_t>(a.B) * ((a.p.max_pages + kPiece - 1) / kPiece);

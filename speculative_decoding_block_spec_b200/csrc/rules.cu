@@ -24,6 +24,7 @@ constexpr int kChunk = 1024;  // tokens of one warp's step over a row: 32 words 
 constexpr int kEditThreads = 512;
 constexpr int kEditTile = 10 * 32 * kEditThreads;  // tokens of the edit kernel's tile: 163,840
 constexpr int kListMax = 4096;  // seen tokens that are taken at a time
+constexpr float kRepMin = 0x1p-100f;  // 2^-100 <= r <= 2^100: 1 / r is a normal number
 constexpr int kRowsMax = SPEC_MAX_K * (SPEC_MAX_L + 1);
 
 template <int DT> __device__ __forceinline__ float load_x(const char* row, int64_t v);
@@ -217,7 +218,7 @@ __device__ __forceinline__ Request load_request(const RulesArgs& a, int b) {
   if (r.ell < 0 || r.ell > a.L) r.flag |= kFlagVerifyLen;
   else if (a.row_off && (r.row0 < 0 || r.row0 + r.nrow > a.n_rows)) r.flag |= kFlagIndex;
   if ((a.h.counts && r.seat >= a.h.seats) || (a.mask && r.m >= a.n_masks)) r.flag |= kFlagIndex;
-  if (!(r.rep > 0.f && r.rep < INFINITY && fabsf(r.freq) < INFINITY && fabsf(r.pres) < INFINITY)) r.flag |= kFlagParam;
+  if (!(r.rep >= kRepMin && r.rep <= 1.f / kRepMin && fabsf(r.freq) < INFINITY && fabsf(r.pres) < INFINITY)) r.flag |= kFlagParam;
   r.pen = r.sat && (r.rep != 1.f || r.freq != 0.f || r.pres != 0.f);
   return r;
 }
@@ -561,6 +562,10 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
   }
 }
 
+static size_t edit_shared(int special) {
+  return kEditTile / 4 + kListMax * 8 + static_cast<size_t>(special) * kSpecialBytes;
+}
+
 cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st) {
   RulesArgs a = args;
   const int most = a.K * a.rows;
@@ -583,9 +588,11 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   a.per = (most + z - 1) / z;
   a.special = 32 + a.h.n_bias;
   const dim3 grid(static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));
-  const size_t smem = kEditTile / 4 + kListMax * 8 + static_cast<size_t>(a.special) * kSpecialBytes;
+  const size_t smem = edit_shared(a.special);
   void (*k)(RulesArgs) = dtype == 0 ? k_rules_edit<0> : k_rules_edit<1>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // always the most that a call can need: another host thread may be between its own setting and launch
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(edit_shared(32 + SPEC_MAX_BIAS)));
   return e != cudaSuccess ? e : launch_pdl(k, grid, dim3(kEditThreads), smem, st, a);
 }
 

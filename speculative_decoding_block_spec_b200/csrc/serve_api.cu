@@ -37,7 +37,8 @@ int check_history(const spec_history* h) {
 int check_pages(const spec_kv_pages* p, int B) {
   if (!p || !p->page_table || !p->owned || !p->free_pages || !p->free_count) return SPEC_ERR_ARG;
   if (p->seats < 1 || p->max_pages < 1 || p->n_pages < 1 || p->page_size < 1) return SPEC_ERR_ARG;
-  if (p->seats > SPEC_MAX_SEATS || static_cast<int64_t>(B) * p->max_pages > 0x7fffffff) return SPEC_ERR_UNSUPPORTED;
+  if (p->seats > SPEC_MAX_SEATS || p->max_pages > (1 << 30) || static_cast<int64_t>(B) * p->max_pages > 0x7fffffff)
+    return SPEC_ERR_UNSUPPORTED;
   if (!aligned(p->page_table, 4) || !aligned(p->owned, 4) || !aligned(p->free_pages, 4) || !aligned(p->free_count, 4))
     return SPEC_ERR_ARG;
   return SPEC_OK;

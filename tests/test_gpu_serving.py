@@ -154,6 +154,9 @@ SHAPES = [
     dict(B=3, K=1, L=2, V=65536, rows=3, bias=1024, hist=30, seats=False, vlen=False),
     dict(B=2, K=1, L=1, V=151936, rows=2, bias=64, mask="some", hist=5000),
     dict(B=6, K=1, L=2, V=640, rows=3, bias=6, params=False),           # NULL penalties: biases alone
+    dict(B=2, K=1, L=3, V=200000, rows=4, bias=200, mask="own", hist=6000),     # more than one tile of the vocabulary
+    dict(B=1, K=2, L=2, V=1 << 20, rows=2, bias=30, hist=3000, vlen=False),                 # the largest vocabulary
+    dict(B=1, K=1, L=1, V=20000, rows=2, bias=5, hist=60000, vlen=False),                   # nearly every token seen: several rounds
 ]
 
 
@@ -253,7 +256,7 @@ def test_rules_leave_out_what_they_cannot_do():
     run(lambda c: c.vlen.__setitem__(2, -1), specv.DEV_VERIFY_LEN)
     run(lambda c: c.seats.__setitem__(1, 8), specv.DEV_INDEX)
     run(lambda c: c.mask_rows.__setitem__(3, 2), specv.DEV_INDEX)
-    for v in (0.0, -1.0, np.nan, np.inf):
+    for v in (0.0, -1.0, np.nan, np.inf, 1e-38, 1e38):
         run(put("repetition", 3, v), specv.DEV_PARAM)
     run(put("frequency", 0, np.nan), specv.DEV_PARAM)
     run(put("presence", 4, -np.inf), specv.DEV_PARAM)
@@ -274,6 +277,40 @@ def test_rules_ignore_tokens_behind_the_verify_length():
     c.call(x, workspace=ws)
     check_rows(host(x).reshape(c.x.shape), c.x, ref, "f32")
     assert ws.status() == 0
+
+
+def test_biases_of_one_token_add_up_in_list_order():
+    """A thousand entries of few tokens, also drafted ones: sums in list order, the same in every run."""
+    V, L, n = 5000, 4, 1000
+    g = np.random.default_rng(3)
+    bt = g.integers(0, 7, (1, n)).astype(np.int32) * 600
+    bv = (g.standard_normal((1, n)) * 10.0 ** g.integers(-3, 4, (1, n))).astype(np.float32)
+    sums = np.zeros(V, np.float32)
+    for t, v in zip(bt[0], bv[0]):
+        sums[t] += v                                  # fp32, in list order
+    h = specv.History(torch.zeros((1, V), dtype=I32, device="cuda"), torch.zeros((1, (V + 31) // 32), dtype=I32, device="cuda"),
+                      presence=torch.zeros(1, device="cuda"), repetition=torch.full((1,), 2.0, device="cuda"),
+                      bias_tokens=dev(bt), bias_values=dev(bv))
+    tok = dev(np.array([[600, 1200, 601, 600]], np.int32))
+    first = None
+    for _ in range(5):
+        x = torch.zeros((1, L + 1, V), device="cuda")
+        specv.spec_logit_rules(x, h, draft_tokens=tok)
+        np.testing.assert_array_equal(x[0].cpu().numpy(), np.broadcast_to(sums, (L + 1, V)))
+        assert first is None or torch.equal(first, x)
+        first = x
+
+
+def test_rules_repetition_alone_and_rows_without_a_seat():
+    """NULL frequency and presence: the counts are not needed; a request without a seat is copied as it is."""
+    c = Case(61, 3, 1, 2, 3000, rows=3, dtype="f32", mask="own")
+    del c.kw["frequency"], c.kw["presence"]
+    c.seats[0] = -1
+    x = logits_to_torch(c.x).view(3, 1, 3, 3000)
+    y = torch.full_like(x, 2.0)
+    before = host(y).reshape(c.x.shape).copy()
+    c.call(x, out=y)
+    check_rows(host(y).reshape(c.x.shape), c.x, c.oracle(), "f32", before)
 
 
 def test_rules_neutral_call_writes_nothing():
