@@ -31,15 +31,20 @@ class _CPages(ctypes.Structure):
 
 
 def _check(t, name, dtype, shape, device=None):
-    """Raises unless t is a contiguous tensor of `dtype` and `shape` (None: any size) on device number `device`
-    (-1: host); returns its address. Shapes come first, so a mis-sized tensor is named even where there is no CUDA
-    device."""
+    """Raises unless t is a contiguous tensor of `dtype` and `shape` (a number: that many dimensions of any size; None
+    in it: any size) on device number `device` (-1: host); returns its address. Shapes come first, so a mis-sized
+    tensor is named even where there is no CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
     s = t.shape
-    if s != shape and (len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape))):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(s), tuple("*" if w is None else w for w in shape)))
-    if t.dtype != dtype:
+    if shape.__class__ is int:
+        if len(s) != shape:
+            raise ValueError("%s has shape %s, expected %d dimensions" % (name, tuple(s), shape))
+    elif s != shape:
+        if len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape)):
+            raise ValueError("%s has shape %s, expected %s"
+                             % (name, tuple(s), tuple("*" if w is None else w for w in shape)))
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -182,38 +187,37 @@ def spec_logit_rules(logits, history=None, *, seats=None, draft_tokens=None, ver
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a tensor")
     dev, shape, K = logits.get_device(), logits.shape, 1
-    V = shape[-1] if shape else 0
-    L = None
+    dims = len(shape)
+    V = shape[-1] if dims else 0
+    L = tp = None
     if draft_tokens is not None:
-        if draft_tokens.dim() != 2:
-            raise ValueError("draft_tokens must be [B, L]")
+        tp = _check(draft_tokens, "draft_tokens", _I32, 2, dev)
         B, L = draft_tokens.shape
     if target_row_off is not None:
         if L is None:
             raise ValueError("packed rows need draft_tokens [B, L]")
-        if logits.dim() != 2:
-            raise ValueError("logits has shape %s, expected packed rows [*, V]" % (tuple(logits.shape),))
+        if dims != 2:
+            raise ValueError("logits has shape %s, expected packed rows [*, V]" % (tuple(shape),))
         if target_row_off.dim() != 1 or target_row_off.shape[0] not in (B, B + 1):
             raise ValueError("target_row_off must be [B] or [B + 1] with B = %d" % B)
         rows = L + 1
     else:
-        if logits.dim() not in (3, 4):
-            raise ValueError("logits has shape %s, expected [B, rows, V] or [B, K, rows, V]" % (tuple(logits.shape),))
-        rows = logits.shape[-2]
-        if logits.dim() == 4:
-            K = logits.shape[1]
+        if dims == 4:
+            K = shape[1]
+        elif dims != 3:
+            raise ValueError("logits has shape %s, expected [B, rows, V] or [B, K, rows, V]" % (tuple(shape),))
+        rows = shape[-2]
         if L is None:
-            B, L = logits.shape[0], max(rows - 1, 0)
+            B, L = shape[0], max(rows - 1, 0)
             if history is not None and L > 0:
                 raise ValueError("draft_tokens [B, L]: the history of row i holds the drafted tokens before it")
-        if logits.shape[0] != B or rows not in (L, L + 1):
+        if shape[0] != B or rows not in (L, L + 1):
             raise ValueError("logits has shape %s, expected %d requests of %d (draft) or %d (target) rows"
-                             % (tuple(logits.shape), B, L, L + 1))
+                             % (tuple(shape), B, L, L + 1))
     dt = _dtype_code(logits)
     xp = _check(logits, "logits", logits.dtype, shape, dev)
     op = xp if out is None else _check(out, "out", logits.dtype, shape, dev)
-    tp = None if draft_tokens is None else _check(draft_tokens, "draft_tokens", _I32, (B, L), dev)
-    rp = None if target_row_off is None else _check(target_row_off, "target_row_off", _I32, (None,), dev)
+    rp = None if target_row_off is None else _check(target_row_off, "target_row_off", _I32, 1, dev)
     vp = None if verify_len is None else _check(verify_len, "verify_len", _I32, (B,), dev)
     sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
     hp = None
@@ -248,12 +252,12 @@ def spec_history_add(history, tokens, *, seats=None, offsets=None, output=True, 
     [B + 1] int32. output: generated tokens (counted), else prompt tokens."""
     dev = history._dev
     if offsets is None:
-        tp = _check(tokens, "tokens", _I32, (None, None), dev)
+        tp = _check(tokens, "tokens", _I32, 2, dev)
         B = tokens.shape[0]
         op = None
     else:
-        tp = _check(tokens, "tokens", _I32, (None,), dev)
-        op = _check(offsets, "offsets", _I32, (None,), dev)
+        tp = _check(tokens, "tokens", _I32, 1, dev)
+        op = _check(offsets, "offsets", _I32, 1, dev)
         B = offsets.shape[0] - 1
     sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
     if seats is None and B > history.seats:
@@ -264,7 +268,7 @@ def spec_history_add(history, tokens, *, seats=None, offsets=None, output=True, 
 def spec_history_clear(history, seats, *, workspace=None):
     """Empties the history of seats [B] int32 (negative: skipped)."""
     dev = history._dev
-    sp = _check(seats, "seats", _I32, (None,), dev)
+    sp = _check(seats, "seats", _I32, 1, dev)
     _launch(dev, workspace, 256, "spec_history_clear", history._ref, sp, seats.shape[0])
 
 
@@ -275,7 +279,7 @@ def spec_kv_map(pages, ctx_len, offsets, n_tokens, *, seats=None, block_table=No
     the outputs. block_table [B, max_pages] int32 (None: not written).
     Returns (kv_slots [n_tokens] int64, positions [n_tokens] int32, seq_len [B] int32)."""
     dev = pages._dev
-    cp = _check(ctx_len, "ctx_len", _I32, (None,), dev)
+    cp = _check(ctx_len, "ctx_len", _I32, 1, dev)
     B, N = ctx_len.shape[0], int(n_tokens)
     fp = _check(offsets, "offsets", _I32, (B + 1,), dev)
     sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
@@ -298,7 +302,7 @@ def spec_kv_release(pages, seats, *, keep_len=None, workspace=None):
     """Requests in seats [B] int32 (negative: skipped) give back the pages
     behind their first keep_len [B] int32 tokens (None: all of them)."""
     dev = pages._dev
-    sp = _check(seats, "seats", _I32, (None,), dev)
+    sp = _check(seats, "seats", _I32, 1, dev)
     B = seats.shape[0]
     kp = None if keep_len is None else _check(keep_len, "keep_len", _I32, (B,), dev)
     _launch(dev, workspace, 512, "spec_kv_release", pages._ref, sp, B, kp)
