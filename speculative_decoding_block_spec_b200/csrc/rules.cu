@@ -44,9 +44,11 @@ template <> __device__ __forceinline__ void store_x<1>(char* row, int64_t v, flo
   asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(z));
   reinterpret_cast<unsigned short*>(row)[v] = h;
 }
+template <int DT> struct Bits { using type = uint32_t; };  // elements that are moved, not computed, keep their bits
+template <> struct Bits<1> { using type = unsigned short; };
 template <int DT> __device__ __forceinline__ void copy_x(char* out, const char* in, int64_t v) {
-  if constexpr (DT == 0) reinterpret_cast<float*>(out)[v] = reinterpret_cast<const float*>(in)[v];
-  else reinterpret_cast<unsigned short*>(out)[v] = reinterpret_cast<const unsigned short*>(in)[v];
+  using Raw = typename Bits<DT>::type;
+  reinterpret_cast<Raw*>(out)[v] = reinterpret_cast<const Raw*>(in)[v];
 }
 
 // The -inf pattern of 16 bytes of logits.
@@ -299,12 +301,13 @@ __device__ __forceinline__ Special carve_special(char* base, int n) {
 // The ids of real histories crowd in the low end of the vocabulary, so a
 // block takes all of it (in tiles of kEditTile tokens, one for most models):
 // it compacts the named tokens into a list in shared memory and spreads list x
-// rows over its threads, eight elements in flight per thread. Seen tokens
+// rows over its threads, two elements in flight per thread (four cost 2 % more on 2048 draft
+// rows, eight 11 %: the scattered sectors keep DRAM busy, longer bursts only queue). Seen tokens
 // need their count alone; drafted and biased ones, whose value differs from
 // row to row or has a sum in it, come first in the list and go a slower way.
 template <int DT>
 __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs a) {
-  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 8;  // WPT words of the bit table per thread
+  constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 2;  // WPT words of the bit table per thread
   constexpr int es = Elem<DT>::kBytes;
   extern __shared__ __align__(16) char s_dyn[];
   uint32_t* s_word = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] the tile's seen bits
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
       if (ln == 0 && no == 0) break;
       if (l0) __syncthreads();
       // the token of rank j: a search over the threads' ranks, then over the thread's words, then over the word's bits
-#pragma unroll 2
+#pragma unroll 1
       for (int e = tid; e < ln; e += NT) {
         const int j = l0 + e;
         int lo = 0;
@@ -571,10 +574,10 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   const int most = a.K * a.rows;
   const bool inplace = a.x == a.out;
   if (!inplace || a.mask) {
-    // a row is cut until the grid has 8 blocks for each of the GPU's 148 x 6 slots, 8 chunks (one per warp) at least;
+    // a row is cut until the grid has 4 blocks for each of the GPU's 148 x 6 slots, 8 chunks (one per warp) at least;
     // copies, which have their data to wait for, into those
     const int64_t chunks = (a.V + kChunk - 1) / kChunk, rows = static_cast<int64_t>(a.B) * most;
-    const int64_t cut = std::max<int64_t>(1, std::min<int64_t>((chunks + kWarps - 1) / kWarps, 148 * 48 / rows));
+    const int64_t cut = std::max<int64_t>(1, std::min<int64_t>((chunks + kWarps - 1) / kWarps, 148 * 24 / rows));
     a.per = inplace ? static_cast<int>((chunks + cut - 1) / cut) : kWarps;
     const dim3 grid(static_cast<unsigned>((chunks + a.per - 1) / a.per), static_cast<unsigned>(a.B),
                     static_cast<unsigned>(most));
@@ -584,7 +587,11 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
     if (e != cudaSuccess) return e;
   }
   if (!a.h.counts) return cudaSuccess;
-  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 148 * 3 / a.B)));
+  // Blocks of a request: the GPU's 296 slots filled once, where every row is there; with lengths known on the device
+  // alone, half as many again, as some find no row. 2048 draft rows 52.2 us by 2 blocks per SM, 56.4 by 3; 544 packed
+  // target rows 52.2 and 48.7.
+  const int slots = 148 * (a.vlen ? 3 : 2);
+  const int z = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, slots / a.B)));
   a.per = (most + z - 1) / z;
   a.special = 32 + a.h.n_bias;
   const dim3 grid(static_cast<unsigned>(a.B), static_cast<unsigned>((most + a.per - 1) / a.per));

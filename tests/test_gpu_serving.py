@@ -205,6 +205,34 @@ def test_rules_on_rows_at_odd_addresses(dtype, shift):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [4096, 5000, 4097])
+def test_masks_keep_the_bits_of_what_they_allow(V, dtype):
+    """Rows under masks that allow a few, some, half and nearly all tokens, NaN payloads among the allowed: every
+    allowed element keeps its bits, in place and in the copy."""
+    g = np.random.default_rng(V)
+    B, R = 5, 3
+    x = to_type(g.standard_normal((B * R, V)).astype(np.float32), dtype)
+    if dtype == "bf16":
+        x[:, ::5] = 0x7f81 + (np.arange(x[:, ::5].shape[1]) % 100).astype(np.uint16)
+    else:
+        x.view(np.uint32)[:, ::5] = 0x7f800001 + np.arange(x[:, ::5].shape[1], dtype=np.uint32)
+    ok = g.random((B, R, V)) < np.array([0.0005, 0.02, 0.5, 0.97, 0.9995])[:, None, None]
+    ok[0, 1], ok[4, 1] = False, True
+    ok[0, 2] = False
+    ok[0, 2, [0, 1, 33, 1023, 1024, 2047, V - 1]] = True
+    want = np.where(ok.reshape(B * R, V), x, to_type(np.full(1, -np.inf, np.float32), dtype))
+    words_ = words(plain.pack_bits(ok))
+    t = logits_to_torch(x).view(B, R, V)
+    y = torch.zeros_like(t)
+    specv.spec_logit_rules(t, mask=words_, out=y)
+    specv.spec_logit_rules(t, mask=words_)
+    for got in (y, t):
+        got = host(got).reshape(B * R, V)
+        np.testing.assert_array_equal(got.view(np.uint32 if dtype == "f32" else np.uint16),
+                                      want.view(np.uint32 if dtype == "f32" else np.uint16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rules_on_infinities_and_nan(dtype):
     c = Case(11, 2, 1, 2, 300, rows=3, dtype=dtype, hist=150, bias=4, mask="own", vlen=False, seats=False)
     x = plain.widen(c.x).astype(np.float32)
