@@ -12,9 +12,10 @@ FLAG_TOKEN_RANGE, FLAG_VERIFY_LEN, FLAG_INDEX, FLAG_PARAM, FLAG_PAGES, FLAG_LENG
 def widen(x):
     """Logits as float64 (bf16 bits or float32)."""
     x = np.ascontiguousarray(x)
-    if x.dtype == np.uint16:
-        return (x.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
-    return x.astype(np.float64)
+    with np.errstate(invalid="ignore"):  # signalling NaN patterns
+        if x.dtype == np.uint16:
+            return (x.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+        return x.astype(np.float64)
 
 
 def bits_of(words, V):

@@ -14,6 +14,12 @@
 // memory (a few loads per thread, B <= 4096) and then takes its share of the
 // tokens and of the table entries; the last block to finish writes the new
 // counts, which until then all blocks read. One launch, no grid barrier.
+//
+// Bound by the chain of memory round trips: lengths and seats, pages held,
+// table entries, the ticket. Map and release together: 64 requests of up to
+// 4096 tokens 10.7 us, 1024 of up to 32,768 tokens (a million table entries)
+// 14.1 us, 32 prompts of up to 8192 tokens 11.5 us. With blocks of 256
+// threads, a block to 1024 table entries, the second took 35 us.
 #include <algorithm>
 
 #include "common.cuh"

@@ -9,9 +9,17 @@
 // distribution that plain decoding would have sampled from at that position,
 // so verification against the edited rows stays lossless.
 //
-// Only the tokens that a rule names change. In place, the kernel therefore
-// reads the seen bits (V / 8 bytes per request) and edits the named elements
-// alone; out of place it streams the row once and edits as it goes.
+// Only the tokens that a rule names change. Two kernels, each launched where
+// it has work:
+//  k_rules_stream  what touches whole rows: the mask's -inf, and the copy out
+//    of place. Bound by HBM: 544 rows of 151,936 bf16 tokens are copied in
+//    54.4 us (6.1 TB/s, a plain copy 51.5) and overwritten with -inf in 30.
+//  k_rules_edit    the named elements. It reads the seen bits (V / 8 bytes a
+//    request) and the counts and logits that they name. Bound by scattered
+//    sectors: an edit of 2 bytes moves 64 bytes each way. Reading, changing
+//    and writing 961 Zipf tokens in each of 2048 rows takes 45 us by a kernel
+//    that does nothing else; with bits, counts, drafted and biased tokens it
+//    takes 52 us here.
 #include <algorithm>
 
 #include "common.cuh"
@@ -34,7 +42,7 @@ template <> __device__ __forceinline__ float load_x<0>(const char* row, int64_t 
 template <> __device__ __forceinline__ float load_x<1>(const char* row, int64_t v) {
   return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(row)[v]) << 16);
 }
-// bf16: one rounding to nearest even of the fp32 result (half a step, 2^-9 of the value's binade).
+// bf16: one rounding to nearest even of the fp32 result, at most 2^-8 of the value.
 template <int DT> __device__ __forceinline__ void store_x(char* row, int64_t v, float z);
 template <> __device__ __forceinline__ void store_x<0>(char* row, int64_t v, float z) {
   reinterpret_cast<float*>(row)[v] = z;
@@ -220,7 +228,8 @@ __device__ __forceinline__ Request load_request(const RulesArgs& a, int b) {
   if (r.ell < 0 || r.ell > a.L) r.flag |= kFlagVerifyLen;
   else if (a.row_off && (r.row0 < 0 || r.row0 + r.nrow > a.n_rows)) r.flag |= kFlagIndex;
   if ((a.h.counts && r.seat >= a.h.seats) || (a.mask && r.m >= a.n_masks)) r.flag |= kFlagIndex;
-  if (!(r.rep >= kRepMin && r.rep <= 1.f / kRepMin && fabsf(r.freq) < INFINITY && fabsf(r.pres) < INFINITY)) r.flag |= kFlagParam;
+  if (!(r.rep >= kRepMin && r.rep <= 1.f / kRepMin && fabsf(r.freq) < INFINITY && fabsf(r.pres) < INFINITY))
+    r.flag |= kFlagParam;
   r.pen = r.sat && (r.rep != 1.f || r.freq != 0.f || r.pres != 0.f);
   return r;
 }
@@ -296,15 +305,18 @@ __device__ __forceinline__ Special carve_special(char* base, int n) {
 }
 
 // Block (b, z): rows q0 .. q1 of request b over the whole vocabulary; reads
-// a.x, writes the named tokens of a.out.
+// a.x, writes the named tokens of a.out. COPY: the rows are copied and masked
+// first.
 //
 // The ids of real histories crowd in the low end of the vocabulary, so a
-// block takes all of it (in tiles of kEditTile tokens, one for most models):
-// it compacts the named tokens into a list in shared memory and spreads list x
-// rows over its threads, two elements in flight per thread (four cost 2 % more on 2048 draft
-// rows, eight 11 %: the scattered sectors keep DRAM busy, longer bursts only queue). Seen tokens
-// need their count alone; drafted and biased ones, whose value differs from
-// row to row or has a sum in it, come first in the list and go a slower way.
+// block takes all of it, in tiles of kEditTile tokens, one for most models
+// (256 decoding rows, histories of 4000 tokens: 23 us; by blocks of 8192 and
+// of 32,768 tokens, of which one had most of the work, 40 and 27). It
+// compacts the seen tokens into a list in shared memory and spreads list x
+// rows over its threads, two elements in flight per thread: on 2048 draft
+// rows four cost 2 % more and eight 11 %, as longer bursts of scattered
+// sectors only queue. Drafted and biased tokens, whose value differs from row
+// to row or has a sum in it, are kept apart.
 template <int DT, bool COPY>
 __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs a) {
   constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 2;  // WPT words of the bit table per thread
@@ -490,6 +502,7 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
       if (ln == 0 && no == 0) break;
       if (l0) __syncthreads();
       // the token of rank j: a search over the threads' ranks, then over the thread's words, then over the word's bits
+      // (each word writing its own tokens in a loop over its bits diverges: 1.7 us for 200 tokens, this 0.7)
 #pragma unroll 1
       for (int e = tid; e < ln; e += NT) {
         const int j = l0 + e;
