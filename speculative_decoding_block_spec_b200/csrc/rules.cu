@@ -320,6 +320,7 @@ __device__ __forceinline__ Special carve_special(char* base, int n) {
 template <int DT, bool COPY>
 __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs a) {
   constexpr int NT = kEditThreads, WPT = kEditTile / 32 / NT, kBatch = 2;  // WPT words of the bit table per thread
+  static_assert(WPT <= 16, "the search over a thread's words takes steps of 8, 4, 2, 1");
   constexpr int es = Elem<DT>::kBytes;
   extern __shared__ __align__(16) char s_dyn[];
   uint32_t* s_word = reinterpret_cast<uint32_t*>(s_dyn);              // [WPT * NT] the tile's seen bits
@@ -493,7 +494,11 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
       s_rank[tid] = rank - mine;
       mine = __shfl_sync(0xffffffffu, all, NT / 32 - 1);
     }
-    __syncthreads();  // s_rank, s_word
+    for (int k = 0, to = s_rank[tid]; k < WPT; ++k) {
+      s_claim[tid * WPT + k] = to;
+      to += __popc(s_word[tid * WPT + k]);
+    }
+    __syncthreads();  // s_rank, s_word, s_claim: from here on, ranks of words
 
     // named tokens x rows; the list in rounds of kListMax (one, unless the history is very long)
     const int n = mine, no = s_no;
@@ -510,11 +515,12 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
 #pragma unroll
         for (int step = NT / 2; step > 0; step >>= 1)
           if (s_rank[lo + step] <= j) lo += step;
-        int left = j - s_rank[lo], w = lo * WPT, c = __popc(s_word[w]);
-        while (left >= c) {
-          left -= c;
-          c = __popc(s_word[++w]);
-        }
+        int w = lo * WPT;
+        const int last = w + WPT - 1;
+#pragma unroll
+        for (int step = 8; step > 0; step >>= 1)
+          if (w + step <= last && static_cast<int>(s_claim[w + step]) <= j) w += step;
+        int left = j - static_cast<int>(s_claim[w]);
         uint32_t bits = s_word[w];
         int at = 0;
 #pragma unroll
@@ -602,9 +608,11 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
   RulesArgs a = args;
   const int most = a.K * a.rows;
   const bool inplace = a.x == a.out;
-  // Out of place, with two rows' worth of blocks for each SM, the edit kernel copies its rows itself: the edits find
-  // part of them in L2. 544 rows of 151,936 bf16 tokens: 80.5 us, as two launches 88.5. Fewer rows leave SMs idle.
-  const bool fused = !inplace && a.h.counts && static_cast<int64_t>(a.B) * most >= 148 * 2;
+  // Out of place, many long rows are copied by the edit kernel itself: the edits find part of them in L2. Fewer leave
+  // SMs idle, and short ones most of a block's warps. bf16, 800 tokens of history, one launch / two launches, us:
+  //   1088 rows of 65,536: 67 / 78    512 of 65,536: 38 / 41    300 of 151,936: 54 / 50
+  //   1088 rows of 16,384: 28 / 30    1088 of 8192: 21 / 19     1562 of 1141: 18 / 14
+  const bool fused = !inplace && a.h.counts && static_cast<int64_t>(a.B) * most >= 148 * 3 && a.V >= 16 * kChunk;
   if ((!inplace && !fused) || (inplace && a.mask)) {
     // a row is cut until the grid has 4 blocks for each of the GPU's 148 x 6 slots, 8 chunks (one per warp) at least;
     // copies, which have their data to wait for, into those

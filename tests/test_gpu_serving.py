@@ -156,9 +156,9 @@ SHAPES = [
     dict(B=6, K=1, L=2, V=640, rows=3, bias=6, params=False),           # NULL penalties: biases alone
     dict(B=2, K=1, L=3, V=200000, rows=4, bias=200, mask="own", hist=6000),     # more than one tile of the vocabulary
     dict(B=1, K=2, L=2, V=1 << 20, rows=2, bias=30, hist=3000, vlen=False),                 # the largest vocabulary
-    dict(B=40, K=1, L=8, V=1500, rows=9, bias=5, mask="some"),          # many rows: copied and edited in one kernel
-    dict(B=20, K=4, L=5, V=777, rows=5, hist=300),
-    dict(B=64, K=1, L=7, V=2048, rows=8, packed=True, bias=9, mask="own"),
+    dict(B=40, K=1, L=8, V=1500, rows=9, bias=5, mask="some"),
+    dict(B=30, K=4, L=4, V=16384, rows=4, hist=300, mask="some"),       # many long rows: copied and edited in one kernel
+    dict(B=64, K=1, L=7, V=16391, rows=8, packed=True, bias=9, mask="own"),
     dict(B=1, K=1, L=1, V=20000, rows=2, bias=5, hist=60000, vlen=False),                   # nearly every token seen: several rounds
 ]
 
