@@ -17,8 +17,8 @@
 //
 // Bound by the chain of memory round trips: lengths and seats, pages held,
 // table entries, the ticket. Map and release together: 64 requests of up to
-// 4096 tokens 10.7 us, 1024 of up to 32,768 tokens (a million table entries)
-// 14.1 us, 32 prompts of up to 8192 tokens 11.5 us. With blocks of 256
+// 4096 tokens 10.6 us, 1024 of up to 32,768 tokens (a million table entries)
+// 14.0 us, 32 prompts of up to 8192 tokens 11.3 us. With blocks of 256
 // threads, a block to 1024 table entries, the second took 35 us.
 #include <algorithm>
 

@@ -73,7 +73,7 @@ class Case:
                 ids = g.integers(0, V, hist) if s % 2 else g.integers(0, min(V, 3 * hist + 1), hist)
                 seen[s, ids] = True
                 np.add.at(counts[s], ids[: hist // 2], 1)
-            counts[0, ids[:1]] = 70000
+            counts[0, ids[:1]], seen[0, ids[:1]] = 70000, True
             self.kw.update(counts=counts, seen=plain.pack_bits(seen))
             if params:
                 self.kw.update(repetition=g.uniform(0.7, 1.5, S).astype(np.float32),
