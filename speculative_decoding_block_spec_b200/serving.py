@@ -17,6 +17,7 @@ import torch
 from . import SpecError, Workspace, _dtype_code, lib
 
 _I32, _F32, _I64 = torch.int32, torch.float32, torch.int64
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # spec_dtype
 
 
 class _CHistory(ctypes.Structure):
@@ -139,8 +140,10 @@ def _raw_stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-# the same handle without a Stream object made for it, where torch offers it
+# the same handle without a Stream object made for it, and the current device without a check for CUDA (the tensors
+# are on it), where torch offers them
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(device, workspace, nbytes, name, *args):
@@ -148,7 +151,7 @@ def _launch(device, workspace, nbytes, name, *args):
     workspace, the call gets one of its own."""
     if device < 0:
         raise TypeError("%s: tensors must be CUDA tensors" % name)
-    if torch.cuda.current_device() != device:
+    if _current_device() != device:
         with torch.cuda.device(device):
             return _launch(device, workspace, nbytes, name, *args)
     if workspace is None:
@@ -214,9 +217,12 @@ def spec_logit_rules(logits, history=None, *, seats=None, draft_tokens=None, ver
         if shape[0] != B or rows not in (L, L + 1):
             raise ValueError("logits has shape %s, expected %d requests of %d (draft) or %d (target) rows"
                              % (tuple(shape), B, L, L + 1))
-    dt = _dtype_code(logits)
-    xp = _check(logits, "logits", logits.dtype, shape, dev)
-    op = xp if out is None else _check(out, "out", logits.dtype, shape, dev)
+    dtype = logits.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        dt = _dtype_code(logits)  # raises
+    xp = _check(logits, "logits", dtype, shape, dev)
+    op = xp if out is None else _check(out, "out", dtype, shape, dev)
     rp = None if target_row_off is None else _check(target_row_off, "target_row_off", _I32, 1, dev)
     vp = None if verify_len is None else _check(verify_len, "verify_len", _I32, (B,), dev)
     sp = None if seats is None else _check(seats, "seats", _I32, (B,), dev)
