@@ -387,7 +387,9 @@ size_t spec_kv_workspace_size(int B);
  *               overlap, and every processed row is written whole.
  *   rows        L + 1 (target rows: i = 0..l_b) or L (draft rows: i < l_b),
  *               l_b = verify_len[b] (L if NULL). Rows beyond are left as they
- *               were. A plain decoding step is L = 0, rows = 1, K = 1.
+ *               were. A plain decoding step is L = 0, rows = 1, K = 1. With
+ *               L = 0 and rows = 0 there is nothing to do, and logits and out
+ *               may be NULL.
  *   n_rows      rows of the buffer (B * K * rows when row_off is NULL).
  *   draft_tokens [B, L] int32 (NULL allowed when L == 0 or history is NULL).
  *               A token outside [0, V) raises SPEC_DEV_TOKEN_RANGE and counts

@@ -56,7 +56,8 @@ int spec_logit_rules(const void* logits, void* out, int dtype, const int32_t* ro
                      int rows, int L, int64_t V, const int32_t* draft_tokens, const int32_t* verify_len,
                      const spec_history* history, const int32_t* seats, const uint32_t* mask, int n_masks,
                      int mask_len, const int32_t* mask_rows, void* workspace, size_t ws_bytes, spec_stream_t stream) {
-  if (!logits || !out || (dtype != SPEC_F32 && dtype != SPEC_BF16) || V < 1) return SPEC_ERR_ARG;
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || V < 1) return SPEC_ERR_ARG;
+  if (n_rows != 0 && (!logits || !out)) return SPEC_ERR_ARG;  // the draft rows of an empty block may be NULL
   if (B < 1 || K < 1 || L < 0 || n_rows < 0 || (rows != L && rows != L + 1)) return SPEC_ERR_ARG;
   if (B > SPEC_MAX_B || K > SPEC_MAX_K || L > SPEC_MAX_L || V > SPEC_MAX_V) return SPEC_ERR_UNSUPPORTED;
   if (n_rows > (int64_t{1} << 40)) return SPEC_ERR_UNSUPPORTED;

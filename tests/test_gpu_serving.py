@@ -345,6 +345,24 @@ def test_rules_repetition_alone_and_rows_without_a_seat():
     check_rows(host(y).reshape(c.x.shape), c.x, c.oracle(), "f32", before)
 
 
+def test_empty_blocks_and_batches_of_padding():
+    """The draft rows of an empty block, a step without tokens, a batch of padding: nothing happens, nothing is flagged."""
+    h, ws = specv.History.empty(2, 100, 3), specv.Workspace(256)
+    h.repetition.fill_(2.0)
+    none, pad = torch.empty((3, 0), dtype=I32, device="cuda"), torch.full((3,), -1, dtype=I32, device="cuda")
+    draft = torch.empty((3, 2, 0, 100), device="cuda")
+    assert specv.spec_logit_rules(draft, h, seats=pad, draft_tokens=none, workspace=ws) is draft
+    x = torch.randn((3, 1, 100), device="cuda")
+    before = x.clone()
+    specv.spec_logit_rules(x, h, seats=pad, draft_tokens=none, workspace=ws)
+    specv.spec_history_add(h, torch.zeros((3, 4), dtype=I32, device="cuda"), seats=pad, workspace=ws)
+    specv.spec_history_clear(h, pad, workspace=ws)
+    assert torch.equal(x, before) and int(h.counts.sum()) == 0 and ws.status() == 0
+    kv = Kv(2, 4, 6, 4, 3, 0)
+    kv.map([5, 0, 9], [0, 0, 0, 0], [-1, -1, -1])
+    kv.release([-1, -1, -1], [1, 2, 3])
+
+
 def test_rules_neutral_call_writes_nothing():
     c = Case(5, 2, 1, 2, 500, rows=3, dtype="bf16")
     c.kw["repetition"][:], c.kw["frequency"][:], c.kw["presence"][:] = 1, 0, 0
