@@ -31,13 +31,14 @@ namespace specv {
 constexpr int kKvThreads = 1024, kKvWarps = kKvThreads / 32;
 constexpr int kPiece = 256;                       // table entries of one warp's step, eight to a lane
 constexpr int kPer = SPEC_MAX_B / kKvThreads;     // requests of one thread at most
+constexpr int kPadding = -1, kRefused = -2;       // KvShared::seat of a request without a seat, of one outside the table
 
 struct KvShared {
   int* off;    // [B + 1] map: offsets
   int* scan;   // [B + 1] exclusive scan of the pages needed / released
   int* ctx;    // [B] map: ctx_len
   int* own;    // [B] pages held
-  int* seat;   // [B] seat; negative: nothing to do for this request
+  int* seat;   // [B] seat; negative: nothing to do for this request (map: kPadding or kRefused)
   int* pages;  // [B] map: pages of the request after the step, -1 when refused; release: pages kept
   uint32_t *once, *twice;  // seats that some / more than one request names
 };
@@ -129,9 +130,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) k_kv_map(const KvArgs a) {
     const int o = a.offsets[b], end = a.offsets[b + 1], ctx = a.ctx_len[b];
     int seat = a.seats ? a.seats[b] : b;
     bad |= o < 0 || end < o || end > a.N;
-    if (seat >= a.p.seats) {
+    if (seat < 0) {
+      seat = kPadding;  // every negative seat of the caller's
+    } else if (seat >= a.p.seats) {
       flag |= kFlagIndex;
-      seat = -2;  // refused
+      seat = kRefused;
     }
     s.off[b] = o;
     if (b == B - 1) s.off[B] = end;
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) k_kv_map(const KvArgs a) {
     if (k >= per || b >= B) continue;
     const int seat = s.seat[b], own = s.own[b];
     int pages = -1;
-    if (seat == -1) {
+    if (seat == kPadding) {
       pages = 0;  // no request here
     } else if (seat >= 0) {
       const int64_t total = static_cast<int64_t>(s.ctx[b]) + a.offsets[b + 1] - s.off[b];

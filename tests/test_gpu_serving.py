@@ -775,3 +775,33 @@ def test_two_host_threads_call_at_once():
         ref = c.oracle()
         check_rows(host(x[0]).reshape(c.x.shape), c.x, ref, "bf16")
         assert all(torch.equal(x[0].view(torch.int16), y.view(torch.int16)) for y in x[1:])
+
+
+# ------------------------------------------------------------------ padding
+
+@pytest.mark.parametrize("pad", [-1, -2, -7, -2 ** 31])
+def test_any_negative_seat_is_padding(pad):
+    """Every call takes every negative seat as no seat: nothing is read, written or flagged for it."""
+    kv = Kv(4, 8, 30, 4, 4, 24)
+    kv.map([5, 3, 9, 2], [0, 3, 7, 9, 12], [2, pad, pad, 0])
+    assert kv.out[2].tolist() == [8, 0, 0, 5]
+    kv.map([8, 2 ** 31 - 1, -4, 5], [1, 2, 6, 6, 8], [2, pad, pad, 0])    # whatever stands beside it
+    assert kv.out[2].tolist() == [9, 0, 0, 7]
+    kv.map([0, 0, 0, 0], [0, 4, 8, 12, 16], [pad] * 4)
+    assert kv.out[2].tolist() == [0] * 4
+    kv.release([pad, 2, pad, 0], [-1, 3, 0, 1])
+    kv.release([pad] * 4)
+    c = Case(71, 4, 2, 3, 1000, rows=4, dtype="f32", bias=4, mask="some")
+    c.seats[1] = c.seats[3] = c.mask_rows[0] = pad
+    ref, ws = c.oracle(), specv.Workspace(256)
+    x = c.view(logits_to_torch(c.x))
+    h = c.history()
+    c.call(x, workspace=ws)
+    check_rows(host(x).reshape(c.x.shape), c.x, ref, "f32")
+    before = h.counts.clone(), h.seen.clone()
+    seats = dev(np.full(3, pad, np.int32))
+    specv.spec_history_add(h, torch.ones((3, 5), dtype=I32, device="cuda"), seats=seats, workspace=ws)
+    specv.spec_history_add(h, torch.ones(3000, dtype=I32, device="cuda"), seats=seats, workspace=ws,
+                           offsets=dev(np.array([0, 2500, 2600, 3000], np.int32)))
+    specv.spec_history_clear(h, seats, workspace=ws)
+    assert torch.equal(h.counts, before[0]) and torch.equal(h.seen, before[1]) and ws.status() == ref["flags"] == 0

@@ -198,3 +198,11 @@ def test_plain_history_by_hand():
                                  True)
     assert c[1, 3] == 2 and c[1, 39] == 1 and c.sum() == 3 and s.tolist() == [[0, 0], [8, 128]]
     assert fl == plain.FLAG_TOKEN_RANGE
+
+
+@pytest.mark.parametrize("pad", [-1, -2, -2 ** 31])
+def test_plain_pages_take_every_negative_seat_as_padding(pad):
+    p = plain.Pages(seats=2, max_pages=3, free=[5, 6, 7], page_size=2)
+    r = p.map([1, 2 ** 31 - 1, 0], [0, 1, 3, 4], 4, seats=[1, pad, pad])
+    assert r["seq_len"] == [2, 0, 0] and r["slots"] == [15, -1, -1, -1] and r["flags"] == 0 and p.stack == [5, 6]
+    assert p.release([pad, 1, pad], [-3, 0, 1]) == 0 and p.stack == [5, 6, 7]
