@@ -371,7 +371,17 @@ size_t spec_kv_workspace_size(int B);
 /*
  * spec_logit_rules — penalties, biases and grammar masks on the logit rows of
  * a verify step, before spec_verify_* or spec_softmax_T reads them ([DBLAST]
- * "Assumptions": target and draft are taken under the same sampling filter).
+ * "Assumptions": target probabilities under the sampling filter; lossless for
+ * any proposal).
+ * Which rows: the target rows, always. The draft rows only where the drafter
+ * drew x_i from row i edited in the same way, with x_0..x_{i-1} known (a
+ * drafter that drafts token by token under the rules). The accept test is
+ * min(1, p/q) with the q that x_i came from: a block drafter draws all its
+ * positions from the unedited rows, and its rows stay as they are. Editing
+ * them afterwards changes the output's distribution, and a drafted token that
+ * a mask forbids then has p = q = 0 and no decision (SPEC_DEV_NONFINITE,
+ * accept_len = -1); with the target alone edited it is rejected, and an
+ * allowed token is drawn.
  * For row i of request b, seat s, with x_0.. the drafted tokens:
  *   c(v)  = counts[s,v] + #{k < i : x_k = v}
  *   known = seen[s,v] or v among x_0..x_{i-1}

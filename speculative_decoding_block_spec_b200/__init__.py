@@ -17,7 +17,7 @@ Entry points (same names as the C ABI):
   spec_verify_mixture_top_p(target, draft, mix_w, tokens, u, g, T, top_p, ...)
   spec_verify_window_stats(...), spec_verify_accept(...)   the two verify stages
   dvl_allocate_pack(scores, budget, dense_target=None, packed_target=None)
-  spec_logit_rules(logits, history, ...)                   penalties, biases, grammar masks on the rows of a step
+  spec_logit_rules(logits, history, ...)                   penalties, biases, grammar masks on the target rows of a step
   spec_history_add(history, tokens, ...), spec_history_clear(history, seats)
   spec_kv_map(pages, ctx_len, offsets, n_tokens, ...), spec_kv_release(pages, seats, ...)
 State tables of the last two groups: History, KvPages (serving.py).

@@ -5,9 +5,11 @@
 //   c = counts[s, v] + #{k < i : x_k = v},  known = seen[s, v] or v in x_<i
 //   z = known ? (x > 0 ? x / r : x * r) : x
 //   z = z - f c - p [c > 0] + bias(v);  z = -inf where the mask's bit is 0
-// The drafted prefix x_<i is part of the history of row i: that is the
-// distribution that plain decoding would have sampled from at that position,
-// so verification against the edited rows stays lossless.
+// The drafted prefix x_<i is part of the history of row i: the edited target
+// row is the distribution that plain decoding would have sampled from at that
+// position. Verification keeps it for any proposal q, as long as q is the one
+// that x_i was drawn from: draft rows are edited only where the drafter itself
+// drew x_i from the row edited with x_<i.
 //
 // Only the tokens that a rule names change. Two kernels, each launched where
 // it has work:

@@ -174,7 +174,10 @@ def kv_workspace_size(B):
 
 def spec_logit_rules(logits, history=None, *, seats=None, draft_tokens=None, verify_len=None, target_row_off=None,
                      mask=None, mask_rows=None, out=None, workspace=None):
-    """Penalties, biases and grammar masks on the rows of a verify step.
+    """Penalties, biases and grammar masks on the rows of a verify step: on the
+    target rows, and on draft rows only where the drafter drew each token from
+    the row edited in the same way (a block drafter's rows, which it drew from
+    unedited, stay as they are; include/specv.h says why).
 
     logits  target rows [B, L+1, V], or packed [n, V] with target_row_off [B]
             (or [B + 1]), or draft rows [B, L, V] / [B, K, L, V]; bf16 or fp32.

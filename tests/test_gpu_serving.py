@@ -805,3 +805,136 @@ def test_any_negative_seat_is_padding(pad):
                            offsets=dev(np.array([0, 2500, 2600, 3000], np.int32)))
     specv.spec_history_clear(h, seats, workspace=ws)
     assert torch.equal(h.counts, before[0]) and torch.equal(h.seen, before[1]) and ws.status() == ref["flags"] == 0
+
+
+# ------------------------------------------------- which rows a step edits
+
+@pytest.mark.parametrize("K", [1, 3])
+def test_a_forbidden_draft_is_rejected_with_an_allowed_token(K):
+    """A block drafter drew its tokens from the unedited rows: the target rows alone are edited. A drafted token that
+    the grammar forbids has p = 0 and is rejected, and the terminal token is one that the grammar allows."""
+    B, L, V = 4, 3, 512
+    x = synth.custom(B=B, L=L, V=V, K=K, T=1.0, dtype="f32", seed=5, cid=720)
+    ok = np.random.default_rng(2).random((B, L + 1, V)) < 0.5
+    for b in range(B):
+        ok[b, np.arange(L), x.tokens[b]] = True
+    ok[1, 1, x.tokens[1, 1]] = ok[2, 0, x.tokens[2, 0]] = False
+    u = np.full((B, L), 1e-4, np.float32)                                # every p / q is above it or 0
+    target, draft = logits_to_torch(x.target), logits_to_torch(x.draft)
+    specv.spec_logit_rules(target, draft_tokens=dev(x.tokens), mask=words(plain.pack_bits(ok)))
+    ws = specv.Workspace(specv.verify_workspace_size(B, L, K, V))
+    args = (dev(x.tokens), dev(u), dev(x.g), 1.0)
+    acc, out = (specv.spec_verify_block(target, draft, *args, workspace=ws) if K == 1 else
+                specv.spec_verify_mixture(target, draft, dev(x.mix_w), *args, workspace=ws))
+    acc, out = acc.cpu().numpy(), out.cpu().numpy()
+    assert acc.tolist() == [3, 1, 0, 3] and ws.status() == 0
+    for b in range(B):
+        assert ok[b, np.arange(acc[b] + 1), out[b, :acc[b] + 1]].all()
+    ref = oracle.verify(host(target), x.draft, x.tokens, u, x.g, 1.0, mix_w=x.mix_w, diag=True)
+    check_verify(acc, out, ref)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_the_documented_step(graph):
+    """Allocation, paging, the target's rows, rules on them, verification against the draft rows as they were drawn
+    from, history and release, over several steps; a batch with padding, drafted tokens that a grammar forbids, and
+    requests that get no pages and sit a step out. Launched call by call, or captured once and replayed."""
+    B, L, V, K, S, page, n_pages = 6, 8, 4096, 2, 9, 16, 16
+    budget, T = B * (L + 1) // 2, 1.1
+    g = np.random.default_rng(6)
+    x, d = _step_tables(B, L, V, K, S, page, budget, g)
+    seats_h = np.array([4, 0, -3, 2, 8, 5], np.int32)
+    params = dict(repetition=g.uniform(1, 1.4, S), frequency=g.uniform(0, 0.6, S), presence=g.uniform(0, 0.6, S),
+                  bias_values=g.standard_normal((S, 4)))
+    params = {k: v.astype(np.float32) for k, v in params.items()}
+    params["bias_tokens"] = g.integers(0, V, (S, 4)).astype(np.int32)
+    h = specv.History.empty(S, V, 4)
+    for k, v in params.items():
+        getattr(h, k).copy_(dev(v))
+    pages, model = specv.KvPages.empty(S, 40, n_pages, page), plain.Pages(S, 40, np.arange(n_pages - 1, -1, -1), page)
+    ctx_h = np.array([40, 37, 0, 60, 20, 43], np.int32)
+    off0 = np.concatenate([[0], np.cumsum(ctx_h)]).astype(np.int32)
+    prompts, seats = g.integers(0, V, off0[-1]).astype(np.int32), dev(seats_h)
+    specv.spec_history_add(h, dev(prompts), offsets=dev(off0), seats=seats, output=False)
+    specv.spec_kv_map(pages, torch.zeros(B, dtype=I32, device="cuda"), dev(off0), int(off0[-1]), seats=seats)
+    assert model.map([0] * B, off0, int(off0[-1]), seats_h)["flags"] == 0
+    counts, seen, _ = plain.history_add(np.zeros((S, V), np.int32), np.zeros((S, V // 32), np.uint32), seats_h,
+                                        [prompts[off0[b]:off0[b + 1]] for b in range(B)], False)
+    ok, mrows = g.random((2, L + 1, V)) < 0.7, np.array([-1, 1, -1, 0, -1, 1], np.int32)
+    mask, mask_rows, ctx = words(plain.pack_bits(ok)), dev(mrows), dev(ctx_h)
+    e = lambda *s, dt=I32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    packed = torch.empty((budget, V), dtype=torch.bfloat16, device="cuda")
+    dvl, ver, keep = (e(B), e(B + 1), e(budget)), (e(B), e(B, L + 1)), e(B)
+    kv_out, bt = (e(budget, dt=torch.int64), e(budget), e(B)), torch.full((B, 40), -1, dtype=I32, device="cuda")
+    ws = dict(dvl=specv.Workspace(specv.dvl_workspace_size(B)), ver=specv.Workspace(specv.verify_workspace_size(B, L, K, V)),
+              rules=specv.Workspace(specv.rules_workspace_size(B)), kv=specv.Workspace(specv.kv_workspace_size(B)))
+
+    def step():
+        vl, off, slot_map = specv.dvl_allocate_pack(d["scores"], budget, workspace=ws["dvl"], out=dvl)
+        _, _, seq_len = specv.spec_kv_map(pages, ctx, off, budget, seats=seats, block_table=bt, out=kv_out,
+                                          workspace=ws["kv"])
+        vl.masked_fill_(seq_len < 0, -1)
+        # the target's forward pass over the allocated slots
+        torch.index_select(d["target"].view(-1, V), 0, slot_map.clamp(min=0), out=packed)
+        specv.spec_logit_rules(packed, h, seats=seats, draft_tokens=d["tokens"], verify_len=vl, target_row_off=off,
+                               mask=mask, mask_rows=mask_rows, workspace=ws["rules"])
+        acc, out = specv.spec_verify_mixture(packed, d["draft"], d["mix_w"], d["tokens"], d["u"], d["g"], T,
+                                             verify_len=vl, target_row_off=off[:B], workspace=ws["ver"], out=ver)
+        specv.spec_history_add(h, out, seats=seats, workspace=ws["rules"])
+        torch.add(ctx, acc, out=keep)
+        keep.add_(1)
+        specv.spec_kv_release(pages, seats, keep_len=keep, workspace=ws["kv"])
+        ctx.copy_(keep)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    captured, flags, refused, forbidden = None, dict(dvl=0, ver=0, rules=0, kv=0), 0, 0
+    with torch.cuda.stream(s):
+        if graph:
+            captured = torch.cuda.CUDAGraph()
+            s.synchronize()
+            with torch.cuda.graph(captured, stream=s):
+                step()
+        for trial in range(6):
+            scores = -np.sort(-g.beta(5, 2, (B, L)), axis=1).astype(np.float32)
+            u, toks = g.random((B, L), dtype=np.float32), x.tokens.copy()
+            if trial % 2:
+                toks[:, 1] = toks[:, 0]
+            for k, v in dict(scores=scores, u=u, tokens=toks).items():
+                d[k].copy_(dev(v))
+            captured.replay() if graph else step()
+            s.synchronize()
+            ra = oracle.dvl_allocate(scores, budget)
+            off, r = ra["offsets"], model.map(ctx_h, ra["offsets"], budget, seats_h)
+            np.testing.assert_array_equal(kv_out[0].cpu().numpy(), r["slots"])
+            np.testing.assert_array_equal(kv_out[2].cpu().numpy(), r["seq_len"])
+            vl = np.where(np.array(r["seq_len"]) < 0, -1, ra["verify_len"]).astype(np.int32)
+            dense = host(d["target"]).reshape(-1, V)[np.maximum(ra["slot_map"], 0)]
+            rt = plain.logit_rules(dense, B, 1, L + 1, L, row_off=off[:B], tokens=toks, verify_len=vl, seats=seats_h,
+                                   counts=counts, seen=seen, mask=plain.pack_bits(ok), mask_rows=mrows, **params)
+            check_rows(host(packed), dense, rt, "bf16")
+            ref = oracle.verify(host(packed), x.draft, toks, u, x.g, T, mix_w=x.mix_w, verify_len=vl,
+                                target_row_off=off[:B], diag=True)
+            acc, out = ver[0].cpu().numpy(), ver[1].cpu().numpy()
+            check_verify(acc, out, ref, verify_len=vl)
+            for b in range(B):
+                if vl[b] < 0:
+                    assert acc[b] == -1 and (out[b] == -1).all()         # refused: it sits the step out
+                    refused += 1
+                elif mrows[b] >= 0:
+                    at = np.arange(acc[b] + 1)
+                    assert ok[mrows[b], at, out[b, at]].all()
+                    forbidden += int(not ok[mrows[b], np.arange(vl[b]), toks[b, :vl[b]]].all())
+            counts, seen, _ = plain.history_add(counts, seen, seats_h, out, True)
+            np.testing.assert_array_equal(h.counts.cpu().numpy(), counts)
+            np.testing.assert_array_equal(h.seen.cpu().numpy().view(np.uint32), seen)
+            ctx_h = ctx_h + acc + 1
+            f = model.release(seats_h, ctx_h)
+            assert pages.free_pages[:int(pages.free_count)].tolist() == model.stack
+            np.testing.assert_array_equal(ctx.cpu().numpy(), ctx_h)
+            for k, v in dict(ver=ref["flags"], rules=rt["flags"], kv=r["flags"] | f).items():
+                flags[k] |= v
+    assert refused and forbidden
+    assert flags == dict(dvl=0, ver=specv.DEV_VERIFY_LEN, rules=specv.DEV_VERIFY_LEN, kv=specv.DEV_PAGES)
+    assert {k: w.status() for k, w in ws.items()} == flags
+    del captured

@@ -9,8 +9,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import speculative_decoding_block_spec_b200 as specv
 from oracle import serving as plain
+from speculative_decoding_block_spec_b200 import synth
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 E, I32 = torch.empty, torch.int32
@@ -206,3 +208,72 @@ def test_plain_pages_take_every_negative_seat_as_padding(pad):
     r = p.map([1, 2 ** 31 - 1, 0], [0, 1, 3, 4], 4, seats=[1, pad, pad])
     assert r["seq_len"] == [2, 0, 0] and r["slots"] == [15, -1, -1, -1] and r["flags"] == 0 and p.stack == [5, 6]
     assert p.release([pad, 1, pad], [-3, 0, 1]) == 0 and p.stack == [5, 6, 7]
+
+
+# ------------------------------------- which rows a verify step has to edit
+
+def _edited(x, tokens, ok, **kw):
+    B, L = tokens.shape
+    r = plain.logit_rules(x.reshape(-1, x.shape[-1]), B, 1, x.shape[1], L, tokens=tokens, mask=plain.pack_bits(ok), **kw)
+    return r["z"].astype(np.float32).reshape(x.shape)
+
+
+def test_a_forbidden_draft_is_rejected_when_the_target_alone_is_edited():
+    """The second of three drafted tokens is forbidden. With the target rows edited it is rejected and an allowed token
+    ends the block; with the draft rows edited after the draw both probabilities are 0, and there is no decision."""
+    x = synth.custom(B=1, L=3, V=64, T=1.0, dtype="f32", seed=9, cid=721)
+    ok = np.ones((1, 4, 64), bool)
+    ok[0, 1, x.tokens[0, 1]] = False
+    u = np.zeros((1, 3), np.float32)
+    target, draft = _edited(x.target, x.tokens, ok), _edited(x.draft, x.tokens, ok)
+    r = oracle.verify(target, x.draft, x.tokens, u, x.g, 1.0)
+    assert r["accept_len"].tolist() == [1] and r["flags"] == 0 and r["out_tokens"][0, 0] == x.tokens[0, 0]
+    assert r["out_tokens"][0, 1] >= 0 and ok[0, 1, r["out_tokens"][0, 1]]
+    r = oracle.verify(target, draft, x.tokens, u, x.g, 1.0)
+    assert r["accept_len"].tolist() == [-1] and r["flags"] == specv.DEV_NONFINITE
+
+
+def test_edited_target_rows_against_the_proposal_as_drawn_are_lossless():
+    """Blocks of two tokens drawn from fixed rows q; penalties and a mask on the target rows. The first token follows the
+    edited row 0, the second, where the first was accepted as a, the edited row 1 of prefix a: each frequency within 5
+    standard deviations (at most 63 of them: one outside has a chance of 4e-5). With the draft rows edited after the draw the
+    same statistic is far outside, so it would see the error."""
+    g = np.random.default_rng(11)
+    V, N = 8, 60000
+    t, q = g.standard_normal((3, V)).astype(np.float32), g.standard_normal((2, V)).astype(np.float32)
+    ok = np.ones((3, V), bool)
+    ok[0, 2] = ok[1, 5] = False
+    kw = dict(counts=np.array([[2, 0, 0, 1, 0, 0, 0, 0]], np.int32), repetition=[1.6], frequency=[0.4], presence=[0.8],
+              seen=plain.pack_bits(np.array([[True, True, False, True] + [False] * 4])))
+    pairs = np.array([(a, b) for a in range(V) for b in range(V)], np.int32)
+    one = dict(kw, seats=np.zeros(len(pairs), np.int32), mask_rows=np.zeros(len(pairs), np.int32))
+    et = _edited(np.broadcast_to(t, (V * V, 3, V)), pairs, ok[None], **one)
+    eq = _edited(np.broadcast_to(q, (V * V, 2, V)), pairs, ok[None], **one)
+
+    def softmax(z):
+        w = np.exp(z.astype(np.float64) - z.max(-1, keepdims=True))
+        return w / w.sum(-1, keepdims=True)
+
+    draw = [g.choice(V, N, p=softmax(q[i])) for i in range(2)]
+    tokens, at = np.stack(draw, 1).astype(np.int32), draw[0] * V + draw[1]
+    u = g.random((N, 2), dtype=np.float32)
+    gumbel = -np.log(-np.log(g.random((N, 3, V)))).astype(np.float32)
+
+    def worst(draft):
+        r = oracle.verify(et[at], draft, tokens, u, gumbel, 1.0)
+        first, second = r["out_tokens"][:, 0], r["out_tokens"][:, 1]
+        p0, z = softmax(et[0, 0]), []
+        groups = [(first[first >= 0], p0)]
+        for a in range(V):
+            groups.append((second[(r["accept_len"] >= 1) & (first == a)], softmax(et[a * V, 1])))
+        for got, p in groups:
+            n = len(got)
+            if n >= 2000:
+                freq = np.bincount(got, minlength=V) / n
+                assert (freq[p == 0] == 0).all()
+                z += list(np.abs(freq - p)[p > 0] / np.sqrt(p * (1 - p) / n)[p > 0])
+        return max(z), len(z)
+
+    z, n = worst(np.broadcast_to(q, (N, 2, V)).copy())
+    assert z < 5 and n <= 63, (z, n)
+    assert worst(eq[at])[0] > 20
