@@ -392,9 +392,11 @@ size_t spec_kv_workspace_size(int B);
  * bias list that name one token add up in list order.
  *   logits      [B, K, rows, V] of `dtype`, or packed target rows [n_rows, V]
  *               with row_off (K == 1): row (b, i) is row_off[b] + i.
- *   out         same layout; == logits edits in place (only the elements that
- *               a rule changes are written). Otherwise the two must not
- *               overlap, and every processed row is written whole.
+ *   out         same layout; == logits edits in place. Otherwise the two must
+ *               not overlap, and every processed row is written whole. Either
+ *               way elements that no rule changes keep their bits, NaN
+ *               payloads among them: with r = 1, tokens that only the prompt
+ *               holds are such elements.
  *   rows        L + 1 (target rows: i = 0..l_b) or L (draft rows: i < l_b),
  *               l_b = verify_len[b] (L if NULL). Rows beyond are left as they
  *               were. A plain decoding step is L = 0, rows = 1, K = 1. With

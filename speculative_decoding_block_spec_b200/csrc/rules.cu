@@ -568,12 +568,11 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
             const int extra = __popc(sp.drafted[o] & (i >= 32 ? 0xffffffffu : (1u << i) - 1u));
             const int c = max(sp.count[o], 0) + extra;
             const bool known = sp.count[o] >= 0 || extra > 0;
-            const float add = sp.add[o];
-            if ((!known && add == 0.f) || l0) continue;
+            const float add = sp.add[o], minus = freq * static_cast<float>(c) + (c > 0 ? pres : 0.f);
+            if (((!known || rep == 1.f) && minus == 0.f && add == 0.f) || l0) continue;  // x stays, bit by bit
             if (m >= 0 && !(mask[i * W + w0 + (v >> 5)] >> (v & 31) & 1)) continue;
             const float g = load_x<DT>(x + s_off[row], v);
-            store_x<DT>(y + s_off[row], v, (known ? g * (g > 0.f ? inv : rep) : g) -
-                                               (freq * static_cast<float>(c) + (c > 0 ? pres : 0.f)) + add);
+            store_x<DT>(y + s_off[row], v, (known ? g * (g > 0.f ? inv : rep) : g) - minus + add);
           }
 #pragma unroll 1
           for (int j = tid; j < ln; j += 4 * NT) {
@@ -588,7 +587,9 @@ __global__ void __launch_bounds__(kEditThreads, 2) k_rules_edit(const RulesArgs 
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          if (on >> k & 1) store_x<DT>(y + s_off[q2], s_list[e2], f[k] * (f[k] > 0.f ? inv : rep) - s_minus[e2]);
+          // with r = 1 tokens that are not counted stay, bit by bit (x * 1 - 0 would lose a NaN's payload)
+          if ((on >> k & 1) && (rep != 1.f || s_minus[e2] != 0.f))
+            store_x<DT>(y + s_off[q2], s_list[e2], f[k] * (f[k] > 0.f ? inv : rep) - s_minus[e2]);
           q2 += dq;
           e2 += de;
           if (e2 >= ln) {

@@ -938,3 +938,42 @@ def test_the_documented_step(graph):
     assert flags == dict(dvl=0, ver=specv.DEV_VERIFY_LEN, rules=specv.DEV_VERIFY_LEN, kv=specv.DEV_PAGES)
     assert {k: w.status() for k, w in ws.items()} == flags
     del captured
+
+
+# ---------------------------------------------- elements that stay as they are
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,V", [(3, 5000), (150, 16384)])
+def test_elements_that_no_rule_changes_keep_their_bits(B, V, dtype):
+    """With r = 1 a token that only the prompt holds is not changed, although the penalties are on: NaN payloads and
+    signed zeros stay, in place, in the copy, and where rows are copied and edited in one kernel."""
+    L = 2
+    c = Case(81, B, 1, L, V, rows=L + 1, dtype=dtype, hist=400, bias=6, vlen=False)
+    c.kw["repetition"][:] = 1
+    nan = np.arange(c.x[:, ::3].shape[1])
+    if dtype == "bf16":
+        c.x[:, ::3], c.x[:, 1::3] = 0x7f81 + (nan % 100).astype(np.uint16), 0x8000
+    else:
+        c.x.view(np.uint32)[:, ::3], c.x[:, 1::3] = 0x7f800001 + nan.astype(np.uint32), -0.0
+    changed = np.zeros(c.x.shape, bool)
+    prompt_only = 0
+    for b in range(B):
+        s = c.seats[b]
+        for i in range(L + 1):
+            if s < 0:
+                continue
+            row = changed[b * (L + 1) + i]
+            row[c.kw["counts"][s] > 0] = True
+            row[c.tokens[b, :i]] = True
+            row[c.kw["bias_tokens"][s][c.kw["bias_tokens"][s] >= 0]] = True
+            prompt_only += int((plain.bits_of(c.kw["seen"][s], V) & ~row)[::3].sum())
+    assert prompt_only > 50 * B
+    raw = np.uint16 if dtype == "bf16" else np.uint32
+    x = c.view(logits_to_torch(c.x))
+    y = torch.zeros_like(x)
+    c.call(x, out=y)
+    c.call(x)
+    for got in (y, x):
+        got = host(got).reshape(c.x.shape).view(raw)
+        np.testing.assert_array_equal(got[~changed], c.x.view(raw)[~changed])
+    assert torch.equal(x.view(torch.int16 if dtype == "bf16" else I32), y.view(torch.int16 if dtype == "bf16" else I32))
