@@ -17,7 +17,11 @@
  * workspace of at least the size its *_workspace_size function returns.
  * It must be zeroed once (spec_workspace_init) before its first use; after
  * that it is self-resetting, so one fixed-address workspace serves every
- * later call and every replay of a captured CUDA graph. Word 0 of the
+ * later call of the same function at the same sizes (rows; B, L, K, V) and
+ * every replay of a captured CUDA graph. Another function, or other sizes,
+ * take a workspace of their own, or the same one after another
+ * spec_workspace_init: the verify calls keep state where other calls have
+ * scratch. Calls that may share are named with them. Word 0 of the
  * workspace is a sticky device status: the OR of SPEC_DEV_* flags raised by
  * any call since the last spec_workspace_init. It is readable after the
  * stream is synchronised. Calls that overlap on the GPU must not share a
@@ -361,10 +365,13 @@ typedef struct {
   int32_t page_size;          /* tokens of a page, any positive number */
 } spec_kv_pages;
 
-/* Workspaces (spec_workspace_init once, then reused). That of the rules and
- * history calls holds the status word alone, so overlapping calls and graphs
- * may share it; that of the kv calls also holds a ticket and may not be
- * shared by calls that overlap. 0 for B outside 1 ... SPEC_MAX_B. */
+/* Workspaces (spec_workspace_init once, then reused, at any sizes). The rules,
+ * history and kv calls use the first 256 bytes alone, which no other call
+ * uses as scratch: any workspace that is large enough serves them, whatever
+ * used it before. The rules and history calls use the status word alone, so
+ * overlapping calls and graphs may share it; the kv calls also use a ticket
+ * and may not share one while they overlap. 0 for B outside
+ * 1 ... SPEC_MAX_B. */
 size_t spec_rules_workspace_size(int B);
 size_t spec_kv_workspace_size(int B);
 

@@ -121,7 +121,9 @@ def dvl_workspace_size(B):
 
 
 class Workspace:
-    """A caller-owned, fixed-address device workspace, zeroed once at creation."""
+    """A caller-owned, fixed-address device workspace, zeroed once at creation.
+    It serves one function at one set of sizes; the serving calls take any
+    that is large enough (include/specv.h)."""
 
     def __init__(self, nbytes, device=None):
         if nbytes <= 0:

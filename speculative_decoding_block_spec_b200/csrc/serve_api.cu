@@ -7,8 +7,10 @@ using namespace specv;
 
 namespace {
 
-constexpr size_t kStatusBytes = 256;  // status word + padding
-constexpr size_t kTicketBytes = 256;
+constexpr size_t kStatusBytes = 256;  // header: status word + padding
+// The kv calls' ticket lies in the header, where no call has scratch: it stays 0 between calls whatever else used the
+// workspace. (The 256 bytes that spec_kv_workspace_size asks for behind the header are not used.)
+constexpr size_t kTicketAt = 128, kKvBytes = kStatusBytes + 256;
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }  // NULL is aligned
 int map_cuda(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
@@ -50,7 +52,7 @@ extern "C" {
 
 size_t spec_rules_workspace_size(int B) { return B < 1 || B > SPEC_MAX_B ? 0 : kStatusBytes; }
 
-size_t spec_kv_workspace_size(int B) { return B < 1 || B > SPEC_MAX_B ? 0 : kStatusBytes + kTicketBytes; }
+size_t spec_kv_workspace_size(int B) { return B < 1 || B > SPEC_MAX_B ? 0 : kKvBytes; }
 
 int spec_logit_rules(const void* logits, void* out, int dtype, const int32_t* row_off, int64_t n_rows, int B, int K,
                      int rows, int L, int64_t V, const int32_t* draft_tokens, const int32_t* verify_len,
@@ -159,7 +161,7 @@ int spec_kv_map(const spec_kv_pages* pages, const int32_t* seats, int B, const i
   a.seq_len = seq_len;
   a.block_table = block_table;
   a.status = static_cast<int*>(workspace);
-  a.ticket = reinterpret_cast<int*>(static_cast<char*>(workspace) + kStatusBytes);
+  a.ticket = reinterpret_cast<int*>(static_cast<char*>(workspace) + kTicketAt);
   return map_cuda(launch_kv_map(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -178,7 +180,7 @@ int spec_kv_release(const spec_kv_pages* pages, const int32_t* seats, int B, con
   a.B = B;
   a.ctx_len = keep_len;
   a.status = static_cast<int*>(workspace);
-  a.ticket = reinterpret_cast<int*>(static_cast<char*>(workspace) + kStatusBytes);
+  a.ticket = reinterpret_cast<int*>(static_cast<char*>(workspace) + kTicketAt);
   return map_cuda(launch_kv_release(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -977,3 +977,29 @@ def test_elements_that_no_rule_changes_keep_their_bits(B, V, dtype):
         got = host(got).reshape(c.x.shape).view(raw)
         np.testing.assert_array_equal(got[~changed], c.x.view(raw)[~changed])
     assert torch.equal(x.view(torch.int16 if dtype == "bf16" else I32), y.view(torch.int16 if dtype == "bf16" else I32))
+
+
+# ------------------------------------------------------- workspaces, launches
+
+def test_kv_calls_on_a_workspace_that_other_calls_used():
+    """The kv calls keep their ticket where no call has scratch: what a softmax or a history call left in the
+    workspace does not matter."""
+    B = 200
+    ws = specv.Workspace(max(specv.kv_workspace_size(B), specv.softmax_workspace_size(64)))
+    kv = Kv(B, 40, 9000, 16, B, 6000)                                    # several blocks each
+    kv.ws = ws
+    x = torch.randn((64, 4096), device="cuda")
+    g = np.random.default_rng(4)
+    seats = g.permutation(B)
+    h = specv.History.empty(4, 100)
+
+    def others():
+        specv.softmax_T(x, 1.0, workspace=ws)
+        specv.spec_history_add(h, torch.ones((4, 3), dtype=I32, device="cuda"), workspace=ws)
+        assert int(ws.buf[256:260].view(I32)) != 0
+
+    for _ in range(3):
+        others()
+        kv.map(g.integers(0, 500, B), np.concatenate([[0], np.cumsum(g.integers(0, 30, B))]), seats)
+        others()
+        kv.release(seats, g.integers(0, 300, B))
