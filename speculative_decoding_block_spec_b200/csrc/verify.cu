@@ -145,7 +145,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_accept_sample(VerifyArgs a, flo
   int32_t* out = a.out_tokens + static_cast<int64_t>(b) * (L + 1);
 
   // ---- 0. inputs that do not come from the statistics kernel: read while it
-  //         finishes (this grid starts early through programmatic launch)
+  //         finishes (this grid starts early through programmatic launch).
+  //         Without drafted positions there is no such kernel in front, and
+  //         the predecessor may be the one that writes the lengths and offsets
+  if (L == 0) pdl_wait();
   int ell = a.vlen ? a.vlen[b] : L;
   const bool bad_len = ell < 0 || ell > L;
   if (bad_len) ell = 0;

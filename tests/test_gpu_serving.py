@@ -1003,3 +1003,47 @@ def test_kv_calls_on_a_workspace_that_other_calls_used():
         kv.map(g.integers(0, 500, B), np.concatenate([[0], np.cumsum(g.integers(0, 30, B))]), seats)
         others()
         kv.release(seats, g.integers(0, 300, B))
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("top_p", [None, 0.9])
+def test_empty_blocks_right_behind_their_allocation(top_p, graph):
+    """L = 0: no statistics run between the allocation and the decision, which must not read the lengths and offsets
+    before they are written. The buffers hold another valid allocation before."""
+    B, V = 500, 256
+    target = torch.zeros((B, V), device="cuda")
+    want = torch.randint(0, V, (B,), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    target[torch.arange(B), want] = 20.0
+    n = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+    vl, off = n(B, dt=I32), n(B + 1, dt=I32)
+    acc, out = n(B, dt=I32), n(B, 1, dt=I32)
+    size = specv.verify_workspace_size if top_p is None else specv.verify_top_p_workspace_size
+    ws, wd = specv.Workspace(size(B, 0, 1, V)), specv.Workspace(specv.dvl_workspace_size(B))
+    draft, tokens, u, gumbel, scores = n(B, 0, V), n(B, 0, dt=I32), n(B, 0), torch.zeros((B, 1, V), device="cuda"), n(B, 0)
+    stale = torch.arange(B, -1, -1, dtype=I32, device="cuda") % B
+
+    def step():
+        specv.dvl_allocate_pack(scores, B, workspace=wd, out=(vl, off, None))
+        args = (target, draft, tokens, u, gumbel, 1.0) + (() if top_p is None else (top_p,))
+        call = specv.spec_verify_block if top_p is None else specv.spec_verify_block_top_p
+        call(*args, verify_len=vl, target_row_off=off[:B], workspace=ws, out=(acc, out))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    captured = None
+    with torch.cuda.stream(s):
+        if graph:
+            captured = torch.cuda.CUDAGraph()
+            s.synchronize()
+            with torch.cuda.graph(captured, stream=s):
+                step()
+        for _ in range(20):
+            vl.zero_()
+            off.copy_(stale)
+            out.fill_(-5)
+            s.synchronize()
+            captured.replay() if graph else step()
+            s.synchronize()
+            assert int((out.view(-1) != want).sum()) == 0 and int(acc.count_nonzero()) == 0
+    assert ws.status() == 0 and wd.status() == 0
+    del captured
