@@ -1047,3 +1047,33 @@ def test_empty_blocks_right_behind_their_allocation(top_p, graph):
             assert int((out.view(-1) != want).sum()) == 0 and int(acc.count_nonzero()) == 0
     assert ws.status() == 0 and wd.status() == 0
     del captured
+
+
+# ----------------------------------- refusals inside steps and in every kernel
+
+@pytest.mark.parametrize("ps,seats,max_pages,n_pages", [(16, 12, 40, 30), (3, 10, 20, 60)])
+def test_kv_steps_with_refusals(ps, seats, max_pages, n_pages):
+    """Steps in which some requests find no page left, or need more than a row holds, between others that grow, shrink
+    and finish."""
+    g = np.random.default_rng(ps)
+    B, N = 8, 500
+    kv = Kv(seats, max_pages, n_pages, ps, B, N)
+    ctx = np.zeros(seats, np.int64)
+    flags, mixed = [], 0
+    for step in range(30):
+        batch = g.permutation(seats)[:B].astype(np.int32)
+        batch[g.random(B) < 0.1] = -1 - step
+        new = np.where(g.random(B) < 0.3, g.integers(0, 62, B), g.integers(0, 18, B))
+        c = np.where(batch >= 0, ctx[np.maximum(batch, 0)], 0)
+        r = kv.map(c, np.concatenate([[0], np.cumsum(new)]), batch)
+        flags.append(r["flags"])
+        got = np.array(r["seq_len"])
+        mixed += bool((got < 0).any() and ((got > c) & (batch >= 0)).any())
+        keep = np.where(got > 0, np.minimum(got, c + g.integers(0, 30, B)), c)
+        kv.release(batch, keep)
+        ctx[batch[batch >= 0]] = keep[batch >= 0]
+        done = batch[(g.random(B) < 0.1) & (batch >= 0)]
+        if len(done):
+            kv.release(done)
+            ctx[done] = 0
+    assert set(flags) == {0, specv.DEV_PAGES} and mixed > 3
