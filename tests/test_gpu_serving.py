@@ -1077,3 +1077,59 @@ def test_kv_steps_with_refusals(ps, seats, max_pages, n_pages):
             kv.release(done)
             ctx[done] = 0
     assert set(flags) == {0, specv.DEV_PAGES} and mixed > 3
+
+
+def test_refusals_where_rows_are_copied_and_edited_in_one_kernel():
+    """Out of place, 450 rows of 16,391 tokens: a request of each impossible kind keeps its rows."""
+    base = dict(B=150, K=1, L=2, V=16391, rows=3, dtype="bf16", bias=5, mask="some", hist=20)
+    S = 153
+
+    def run(change, want, packed=False):
+        c = Case(23, packed=packed, **base)
+        c.seats, c.mask_rows = np.arange(150, dtype=np.int32), np.arange(150, dtype=np.int32) % 75
+        change(c)
+        ref, ws = c.oracle(), specv.Workspace(256)
+        assert ref["flags"] == want
+        x = c.view(logits_to_torch(c.x))
+        y = torch.full_like(x, 3.0)
+        before = host(y).reshape(c.x.shape).copy()
+        c.call(x, out=y, workspace=ws)
+        check_rows(host(y).reshape(c.x.shape), c.x, ref, "bf16", before)
+        assert ws.status() == want
+
+    run(lambda c: (c.vlen.__setitem__(20, 3), c.vlen.__setitem__(149, -1)), specv.DEV_VERIFY_LEN)
+    run(lambda c: (c.seats.__setitem__(1, S), c.seats.__setitem__(2, -9)), specv.DEV_INDEX)
+    run(lambda c: (c.mask_rows.__setitem__(77, 75), c.mask_rows.__setitem__(3, -4)), specv.DEV_INDEX)
+    run(lambda c: (c.kw["repetition"].__setitem__(8, np.nan), c.kw["presence"].__setitem__(9, np.inf)), specv.DEV_PARAM)
+    run(lambda c: (c.row_off.__setitem__(0, -1), c.row_off.__setitem__(4, c.x.shape[0] - c.vlen[4])), specv.DEV_INDEX,
+        packed=True)
+    run(lambda c: (c.vlen.fill(2), c.tokens.__setitem__((1, 0), 16391), c.kw["bias_tokens"].__setitem__((2, 1), 16391)),
+        specv.DEV_TOKEN_RANGE)
+
+
+def test_two_tiles_where_rows_are_copied_and_edited_in_one_kernel():
+    """450 rows of 163,910 tokens, 70 of them in a second tile of the edit kernel, with seen, drafted and biased tokens in
+    both: the copy has the bits of the form in place, and that follows the definition."""
+    B, L, V = 150, 2, 163910
+    c = Case(24, B, 1, L, V, rows=L + 1, hist=300, bias=8)
+    g = np.random.default_rng(1)
+    c.tokens = np.where(g.random((B, L)) < 0.5, V - 1 - g.integers(0, 70, (B, L)), c.tokens).astype(np.int32)
+    bt = c.kw["bias_tokens"]
+    bt[:, 1:4] = V - 1 - g.integers(0, 70, bt[:, 1:4].shape)
+    bits = plain.bits_of(c.kw["seen"][:, -3:], 70)
+    high = g.random(bits.shape) < 0.3
+    c.kw["seen"][:, -3:] = plain.pack_bits(bits | high)
+    x = c.view(logits_to_torch(c.x))
+    y = torch.full_like(x, 2.0)
+    ws = specv.Workspace(256)
+    c.call(x, out=y, workspace=ws)
+    c.call(x, workspace=ws)
+    done = torch.arange(L + 1, device="cuda")[None, None, :, None] <= dev(c.vlen)[:, None, None, None]
+    assert torch.equal(y.view(torch.int16), torch.where(done, x, torch.full_like(x, 2.0)).view(torch.int16))
+    got = host(x).reshape(c.x.shape)
+    for b in (0, 1, 2, 77, 149):
+        rows = slice(b * (L + 1), (b + 1) * (L + 1))
+        ref = plain.logit_rules(c.x[rows], 1, 1, L + 1, L, tokens=c.tokens[b:b + 1], verify_len=c.vlen[b:b + 1],
+                                seats=c.seats[b:b + 1], **c.kw)
+        check_rows(got[rows], c.x[rows], ref, "bf16")
+    assert ws.status() == 0
