@@ -1133,3 +1133,29 @@ def test_two_tiles_where_rows_are_copied_and_edited_in_one_kernel():
                                 seats=c.seats[b:b + 1], **c.kw)
         check_rows(got[rows], c.x[rows], ref, "bf16")
     assert ws.status() == 0
+
+
+def test_flags_of_calls_on_two_streams_are_collected():
+    """Two calls at once read one history through seats of their own, share a workspace and raise different flags."""
+    V = 20000
+    a, b = (Case(43 + k, 6, 1, 3, V, rows=4, dtype="f32", bias=8) for k in range(2))
+    b.kw = {k: v.copy() for k, v in a.kw.items()}
+    a.seats, b.seats = np.array([0, 1, 2, 3, 0, -1], np.int32), np.array([4, 5, 6, 7, 8, 4], np.int32)
+    b.kw["frequency"][6] = a.kw["frequency"][6] = np.nan
+    a.vlen[2], a.vlen[3] = -1, 4
+    refs, ws = [c.oracle() for c in (a, b)], specv.Workspace(256)
+    assert [r["flags"] for r in refs] == [specv.DEV_VERIFY_LEN, specv.DEV_PARAM]
+    h, start = a.history(), [logits_to_torch(c.x).view(6, 1, 4, V) for c in (a, b)]
+    args = [dict(seats=dev(c.seats), draft_tokens=dev(c.tokens), verify_len=dev(c.vlen)) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(40):
+        xs = [x.clone() for x in start]
+        ws.init()
+        torch.cuda.synchronize()
+        for s, x, k in zip(streams, xs, args):
+            with torch.cuda.stream(s):
+                specv.spec_logit_rules(x, h, workspace=ws, **k)
+        torch.cuda.synchronize()
+        assert ws.status() == specv.DEV_VERIFY_LEN | specv.DEV_PARAM
+        for c, x, r in zip((a, b), xs, refs):
+            check_rows(host(x).reshape(c.x.shape), c.x, r, "f32")
