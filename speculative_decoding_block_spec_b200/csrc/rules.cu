@@ -17,11 +17,11 @@
 //    of place. Bound by HBM: 544 rows of 151,936 bf16 tokens are copied in
 //    54.4 us (6.1 TB/s, a plain copy 51.5) and overwritten with -inf in 30.
 //  k_rules_edit    the named elements. It reads the seen bits (V / 8 bytes a
-//    request) and the counts and logits that they name. Bound by scattered
-//    sectors: an edit of 2 bytes moves 64 bytes each way. Reading, changing
-//    and writing 961 Zipf tokens in each of 2048 rows takes 45 us by a kernel
-//    that does nothing else; with bits, counts, drafted and biased tokens it
-//    takes 52 us here.
+//    request) and the counts and logits that they name. Its time goes into
+//    waiting for scattered loads: 2048 draft rows with about 1000 named tokens
+//    each take 53 us, in which DRAM delivers 117 MB for 4 MB of elements, at
+//    38 % of its rate. With r = 1 only counted, drafted and biased tokens are
+//    written: 39 us. Ids spread evenly share fewer lines: 118 and 79 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -310,10 +310,13 @@ __device__ __forceinline__ Special carve_special(char* base, int n) {
 // a.x, writes the named tokens of a.out. COPY: the rows are copied and masked
 // first.
 //
-// The ids of real histories crowd in the low end of the vocabulary, so a
-// block takes all of it, in tiles of kEditTile tokens, one for most models
-// (256 decoding rows, histories of 4000 tokens: 22.9 us; by blocks of 8192 and
-// of 32,768 tokens, of which one had most of the work, 40 and 27). It
+// A block takes the whole vocabulary, in tiles of kEditTile tokens, one for
+// vocabularies up to 163,840. Measured with log-uniform ids (a vocabulary
+// ordered by frequency), 256 decoding rows, histories of 4000 tokens: 23 us;
+// by blocks of 8192 and of 32,768 tokens, of which one had most of the work,
+// 40 and 27. With ids spread evenly, where such blocks would have had equal
+// work, only this form was measured: 40 us. Each further tile builds a list of
+// its own: 23.8 us at V = 163,840, 26.2 at 163,841, 30.7 at 262,144. A block
 // compacts the seen tokens into a list in shared memory and spreads list x
 // rows over its threads, two elements in flight per thread: on 2048 draft
 // rows four cost 2 % more and eight 11 %, as longer bursts of scattered
@@ -655,12 +658,15 @@ cudaError_t launch_logit_rules(const RulesArgs& args, int dtype, cudaStream_t st
 //  offsets == NULL: tokens is [B, width].
 // Negative tokens are padding.
 //
-// A block takes 1024 tokens. A prompt names a few low ids again and again (3
-// in 10 tokens of a Zipf vocabulary of 152 K fall into one word of the
-// bits), and atomics on one address queue up: a block whose tokens belong to
-// one request first collects the bits of the ids below kHot in shared memory
-// and then writes each word once. 32 prompts of up to 8192 tokens, with
-// clearing their seats: 10.9 us by global atomics alone, 8.8 so.
+// A block takes 1024 tokens. Atomics on one address queue up, and a prompt may
+// name a few ids again and again: a block whose tokens belong to one request
+// first collects the bits of the ids below kHot in shared memory and then
+// writes each word once. 32 prompts of up to 8192 tokens, with clearing their
+// seats, us by global atomics alone / so:
+//   one id throughout            13.2 / 6.8
+//   log-uniform ids of 151,936    9.5 / 8.7    of 262,144   11.1 / 11.8
+//   ids spread evenly             8.7 / 9.5    of 262,144   12.3 / 13.6
+// It is kept for the first line: what a prompt repeats is the user's choice.
 constexpr int kAddTokens = 4;     // per thread
 constexpr int kHot = 32 * 2 * kThreads;
 
